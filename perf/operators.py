@@ -213,11 +213,12 @@ def prepare(case, seed):
             return s
         s["cache"] = qg.KV8Cache(s["codes"], s["scales"], s["table"], s["block"])
         s["out"] = torch.empty_like(s["q"])
+        cu = s["cu"] if case["new"] > 1 else None  # one token per sequence needs no offsets
         if case["op"] == "append":
-            s["plan"] = qg.KV8Append(s["cache"], s["k"], s["v"], s["kv_len"], s["cu"], cos=s["cos"], sin=s["sin"],
+            s["plan"] = qg.KV8Append(s["cache"], s["k"], s["v"], s["kv_len"], cu, cos=s["cos"], sin=s["sin"],
                                      rope_style=case["style"], q=s["q"], q_out=s["out"])
         else:
-            s["plan"] = qg.KV8Attention(s["cache"], s["q"], s["kv_len"], s["cu"], out=s["out"],
+            s["plan"] = qg.KV8Attention(s["cache"], s["q"], s["kv_len"], cu, out=s["out"],
                                         window=case["window"], softcap=case["softcap"])
     return s
 
