@@ -8,7 +8,9 @@
  * an fp16 scale and zero point 2 (w = scale * (code - 2)).  Its neighbours are a
  * small-batch variant, a Walsh-Hadamard + codebook (CQ) matvec, a vocabulary
  * projection finished with logit soft-capping and argmax, constrained token
- * selection, a grouped multi-matrix dispatch and a dependent GEMV chain.
+ * selection, a grouped multi-matrix dispatch and a dependent GEMV chain; and what stands
+ * between those products in a decoder layer: a paged 8-bit key-value cache with its
+ * rotated append, attention over it, and the norms around a block.
  *
  * Conventions for every call:
  *  - Pointers named as device buffers are CUDA device pointers owned by the
@@ -87,7 +89,8 @@ int qg_version(void);
  * producer), 4 a copy in flight never landed while stopping, 8 a grid-wide barrier
  * of qgemv_chain ran out, 16 a CTA of qgemv_chain's persistent kernel stopped at a
  * phase boundary because the chain's abort word was set (by a CTA whose wait ran
- * out, or before the call).  Reads and clears the word of the current device;
+ * out, or before the call), 32 a page id or position out of range that a kv8 call
+ * skipped.  Reads and clears the word of the current device;
  * synchronises the device.
  * Returns QG_OK or QG_ERR_CUDA; *code receives the word (0 = no error).
  */
@@ -305,6 +308,178 @@ int qgemv_grouped_noalloc(int bits, const qg_gemv_desc* descs, int count, unsign
 size_t qg_chain_workspace_bytes(const qg_gemv_desc* descs, int count, const int* phase_sizes, int n_phases);
 int qgemv_chain(int bits, const qg_gemv_desc* descs, int count, const int* phase_sizes, int n_phases, void* ws,
                 size_t ws_bytes, unsigned flags, void* stream);
+
+/*
+ * The 8-bit paged key-value cache, what appends to it and what attends over it
+ * (genie-ai-runtime, "v1.3.0 - split-K decode attention"; Gemma WebGPU Engine, "Roadmap":
+ * the decode step's RoPE and cache write, and the attention partials merged by the last
+ * arriver; needle.js, "Experimental resident attention").
+ *
+ * A cache is a pool of pages of page_size tokens:
+ *   k, v      : device uint8 [n_pages][n_kv_heads][page_size][head_dim], one code per value
+ *   k_scale, v_scale : device fp32 [n_pages][n_kv_heads][page_size / scale_block]
+ *   value     = scale of the (block of scale_block tokens, head) * code, the code an int8 in
+ *               [-127, 127] (QG_KV8_INT8) or an OCP 8-bit float (QG_KV8_E4M3)
+ *   page_table : device int32 [batch][max_pages]; token j of sequence b is slot
+ *               j % page_size of page page_table[b][j / page_size]
+ *   head_dim in {64, 128, 256}; page_size a power of two, 16 to 256; scale_block in
+ *   {16, 32, 64}, at most page_size; 1 <= batch <= QG_KV8_MAX_BATCH
+ *   k and v on 16-byte boundaries, the scales on 4-byte ones.
+ * The sequences of a call:
+ *   kv_len    : device int32 [batch], the tokens of each sequence WITH this call's own
+ *   cu_tokens : device int32 [batch + 1], token t of the call belongs to the sequence b
+ *               with cu_tokens[b] <= t < cu_tokens[b+1] (ascending, from 0 to `tokens`; a
+ *               sequence may have none); NULL: tokens == batch, one token per sequence
+ *   token t sits at position kv_len[b] - cu_tokens[b+1] + t of its sequence.
+ * These arrays and the page table are read on the device.  A position or a page id out of
+ * range there is skipped (its token is neither written nor attended to) and sets 32 in the
+ * device error word (qg_device_error).
+ * Rows of a call: [tokens][heads][head_dim] of `dtype`, the heads of a token contiguous and
+ * tokens `*_stride` values apart (a multiple of 16 bytes); bases on 16-byte boundaries.
+ */
+#define QG_KV8_INT8 0
+#define QG_KV8_E4M3 1
+#define QG_DTYPE_F32 0
+#define QG_DTYPE_F16 1
+#define QG_DTYPE_BF16 2
+#define QG_KV8_MAX_BATCH 4096
+
+typedef struct qg_kv8_cache {
+    void* k;
+    void* v;
+    float* k_scale;
+    float* v_scale;
+    const int32_t* page_table;
+    int format; /* QG_KV8_INT8 or QG_KV8_E4M3 */
+    int n_pages;
+    int n_kv_heads;
+    int head_dim;
+    int page_size;
+    int scale_block;
+    int batch;
+    int max_pages; /* row length of page_table */
+} qg_kv8_cache;
+
+/*
+ * kv8_rope_append: new keys and values into the cache, rotated by their position on the way,
+ * and optionally the queries rotated in the same launch.
+ *   rotation: the first rot_dim values of each head (rot_dim % 8 == 0, 0 <= rot_dim <=
+ *     head_dim) in pairs (i, i + rot_dim/2) (QG_ROPE_HALF) or (2i, 2i+1)
+ *     (QG_ROPE_INTERLEAVED): a' = a cos - b sin, b' = b cos + a sin, with cos and sin fp32
+ *     device tables [n_pos][rot_dim/2] (16-byte aligned) at row positions[t] (device int32
+ *     [tokens]), or the token's cache position where positions is NULL.  Each product and
+ *     sum is rounded to fp32 on its own.  cos and sin NULL: no rotation.  v is not rotated.
+ *   cache: per (block, head) and for k and v on their own, a = the largest finite |value| of
+ *     the call's tokens in the block; the scale becomes s' = max(s, fl(a / qmax)) with qmax
+ *     127 or 448, s being the stored scale, or 0 where this call holds the block's first
+ *     token.  New codes are Q(fl(x / s')), the block's other codes become
+ *     Q(fl(fl(code * s) / s')) if the scale grew (all 0 where s is 0), Q rounding to the
+ *     nearest code (ties to even) and saturating; 0 where s' is 0.  An infinite value is
+ *     stored as the largest code, NaN as 0: the cache holds finite values only.  A block
+ *     that the call begins has the slots past its tokens cleared.
+ *   q, q_out : [tokens][n_q_heads][head_dim] (may be the same buffer), rounded once to
+ *     dtype; both NULL: no queries.
+ * Sequences must not share a page that the call writes.
+ */
+#define QG_ROPE_HALF 0
+#define QG_ROPE_INTERLEAVED 1
+
+typedef struct qg_kv8_append_args {
+    const void* k;
+    const void* v;
+    const void* q;
+    void* q_out;
+    const float* cos;
+    const float* sin;
+    const int32_t* positions;
+    const int32_t* kv_len;
+    const int32_t* cu_tokens;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    int tokens;
+    int n_q_heads;
+    int dtype;
+    int rot_dim;
+    int rope_style;
+    int n_pos;
+} qg_kv8_append_args;
+
+int kv8_rope_append(const qg_kv8_cache* cache, const qg_kv8_append_args* args, unsigned flags, void* stream);
+
+/*
+ * kv8_attention: causal attention of the call's tokens over the cache, which already holds
+ * their own keys and values.
+ *   out[t][h] = sum_j w_j v_j,  w = softmax_j(l_j),  l_j = scale * q[t][h] . k_j, or
+ *   softcap * tanh(scale * q . k_j / softcap) where softcap > 0; j runs over the positions
+ *   max(0, p - window + 1) .. p of the sequence (window <= 0: from 0), p being the token's
+ *   own position; query head h reads kv head h / (n_q_heads / n_kv_heads).
+ *   A token that sees nothing (its position out of range) gets 0 and lse -inf.
+ *   q, out : [tokens][n_q_heads][head_dim] of dtype;  n_q_heads a multiple of n_kv_heads
+ *   lse : device fp32 [tokens][n_q_heads], log sum_j exp(l_j), or NULL
+ *   Scores, sums and outputs are accumulated in fp32.  With fp32 rows, queries and
+ *   weights enter the tensor cores as two binary16 pieces (22 bits); with 16-bit rows the
+ *   weights are rounded to binary16 once.
+ *   ws : device workspace of kv8_attention_workspace_bytes() bytes, 16-byte aligned, whose
+ *     first QG_KV8_CTL_BYTES bytes are zero-filled once after allocation; every completed
+ *     call leaves them zero.  Calls sharing a workspace must not overlap on the GPU.
+ *   The result does not depend on timing: sums are taken in a fixed order.
+ */
+#define QG_KV8_CTL_BYTES 4096
+
+typedef struct qg_kv8_attention_args {
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* kv_len;
+    const int32_t* cu_tokens;
+    long long q_stride, out_stride;
+    int tokens;
+    int n_q_heads;
+    int dtype;
+    int window;
+    float scale;
+    float softcap;
+} qg_kv8_attention_args;
+
+size_t kv8_attention_workspace_bytes(int head_dim);
+int kv8_attention(const qg_kv8_cache* cache, const qg_kv8_attention_args* args, void* ws, size_t ws_bytes,
+                  unsigned flags, void* stream);
+
+/*
+ * rmsnorm_gate_residual: what stands between two blocks of a decoder layer, in one pass
+ * (genie-ai-runtime, "What Gemma 4 E2B actually is"; Gemma WebGPU Engine, "Roadmap": the
+ * RMS residual epilogues).  For each of `rows` rows of n values:
+ *   u  = y / sqrt(mean(y^2) + eps) * (w_post + w_offset)     (w_post NULL: u = y)
+ *   h' = (h + gate * u) * res_scale                          (gate NULL: 1; y NULL: h' = h * res_scale)
+ *   z  = h' / sqrt(mean(h'^2) + eps) * (w_pre + w_offset)    (w_pre NULL: no z)
+ * computed in fp32 from the inputs; h' enters z before it is rounded to h_out's type.
+ *   y, gate, z, w_post, w_pre : device, `dtype`;  h, h_out : device, `res_dtype`, fp32 or
+ *     equal to dtype;  rows of y, h, gate, h_out and z are `*_stride` values apart;
+ *     gate_stride 0: one gate of n values for every row
+ *   h_out may be NULL (not stored) or h itself, z may be y itself; they may not overlap
+ *     otherwise
+ *   rows >= 0, 1 <= n <= QG_MAX_NORM_N, any alignment (16-byte aligned rows are faster)
+ */
+#define QG_MAX_NORM_N 32768
+
+typedef struct qg_norm_args {
+    const void* y;
+    const void* h;
+    const void* gate;
+    const void* w_post;
+    const void* w_pre;
+    void* h_out;
+    void* z;
+    long long y_stride, h_stride, gate_stride, h_out_stride, z_stride;
+    int rows;
+    int n;
+    int dtype;
+    int res_dtype;
+    float eps;
+    float w_offset;
+    float res_scale;
+} qg_norm_args;
+
+int rmsnorm_gate_residual(const qg_norm_args* args, unsigned flags, void* stream);
 
 /*
  * Exposed steps, for exactness checks of the integer parts.

@@ -9,6 +9,7 @@ to anything else.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -28,6 +29,16 @@ QG_FLAG_PLAIN = 0x2
 QG_FLAG_CHAIN_PERSISTENT = 0x4
 QG_CHAIN_CTL_BYTES = 256
 QG_CHAIN_MAX_PHASE_K = 32768
+QG_KV8_INT8 = 0
+QG_KV8_E4M3 = 1
+QG_DTYPE_F32 = 0
+QG_DTYPE_F16 = 1
+QG_DTYPE_BF16 = 2
+QG_ROPE_HALF = 0
+QG_ROPE_INTERLEAVED = 1
+QG_KV8_CTL_BYTES = 4096
+QG_KV8_MAX_BATCH = 4096
+QG_MAX_NORM_N = 32768
 
 # every exported function and its ctypes signature (restype, argtypes)
 _u8p = _u16p = _f32p = _i8p = _i32p = _vp = ctypes.c_void_p
@@ -54,6 +65,10 @@ SIGNATURES = {
     "qgemv_grouped_noalloc": (_i, [_i, _vp, _i, _u, _vp]),
     "qg_chain_workspace_bytes": (_sz, [_vp, _i, _vp, _i]),
     "qgemv_chain": (_i, [_i, _vp, _i, _vp, _i, _vp, _sz, _u, _vp]),
+    "kv8_rope_append": (_i, [_vp, _vp, _u, _vp]),
+    "kv8_attention_workspace_bytes": (_sz, [_i]),
+    "kv8_attention": (_i, [_vp, _vp, _vp, _sz, _u, _vp]),
+    "rmsnorm_gate_residual": (_i, [_vp, _u, _vp]),
     "qg_quantize_act": (_i, [_f32p, _i, _i, _i8p, _f32p, _i32p, _vp]),
     "qg_blockdots": (_i, [_i, _u8p, _u8p, _i, _i, _i8p, _i32p, _vp]),
     "qg_read_floor": (_i, [_vp, _sz, _vp, _u, _vp]),
@@ -407,6 +422,316 @@ def vocab_softcap_select(bits, lo, hi, scale, min, x, softcap: float = 30.0, all
                                           _ptr(logprob), _ptr(ws), ws.numel() * ws.element_size(), flags,
                                           _stream(dev)), "vocab_softcap_select")
     return logits, token, logprob
+
+
+# ---------------------------------------------------------------- the cache, attention over it, the block norms
+_DTYPES = {torch.float32: QG_DTYPE_F32, torch.float16: QG_DTYPE_F16, torch.bfloat16: QG_DTYPE_BF16}
+_FORMATS = {torch.int8: QG_KV8_INT8, torch.float8_e4m3fn: QG_KV8_E4M3}
+_I32 = (torch.int32,)
+_ll = ctypes.c_longlong
+
+
+class KV8CacheStruct(ctypes.Structure):
+    """Mirror of ``qg_kv8_cache``."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp), ("format", _i),
+                ("n_pages", _i), ("n_kv_heads", _i), ("head_dim", _i), ("page_size", _i), ("scale_block", _i),
+                ("batch", _i), ("max_pages", _i)]
+
+
+class KV8AppendArgs(ctypes.Structure):
+    """Mirror of ``qg_kv8_append_args``."""
+    _fields_ = [("k", _vp), ("v", _vp), ("q", _vp), ("q_out", _vp), ("cos", _vp), ("sin", _vp), ("positions", _vp),
+                ("kv_len", _vp), ("cu_tokens", _vp), ("k_stride", _ll), ("v_stride", _ll), ("q_stride", _ll),
+                ("q_out_stride", _ll), ("tokens", _i), ("n_q_heads", _i), ("dtype", _i), ("rot_dim", _i),
+                ("rope_style", _i), ("n_pos", _i)]
+
+
+class KV8AttentionArgs(ctypes.Structure):
+    """Mirror of ``qg_kv8_attention_args``."""
+    _fields_ = [("q", _vp), ("out", _vp), ("lse", _vp), ("kv_len", _vp), ("cu_tokens", _vp), ("q_stride", _ll),
+                ("out_stride", _ll), ("tokens", _i), ("n_q_heads", _i), ("dtype", _i), ("window", _i),
+                ("scale", _f), ("softcap", _f)]
+
+
+class NormArgs(ctypes.Structure):
+    """Mirror of ``qg_norm_args``."""
+    _fields_ = [("y", _vp), ("h", _vp), ("gate", _vp), ("w_post", _vp), ("w_pre", _vp), ("h_out", _vp), ("z", _vp),
+                ("y_stride", _ll), ("h_stride", _ll), ("gate_stride", _ll), ("h_out_stride", _ll), ("z_stride", _ll),
+                ("rows", _i), ("n", _i), ("dtype", _i), ("res_dtype", _i), ("eps", _f), ("w_offset", _f),
+                ("res_scale", _f)]
+
+
+def _need_rows(t, name, heads, d, device, dtype=None):
+    """A row tensor [tokens][heads][d] whose heads are contiguous within a token (tokens may be strided)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype or tuple(_DTYPES)}")
+    if t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [tokens][{heads or 'heads'}][{d}]")
+    if t.shape[1] < 1 or (t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d))):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+
+
+def _row_stride(t):
+    """Values between two tokens' (or rows') starts; a lone row has no neighbour to be apart from."""
+    return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])
+
+
+class _Plan:
+    """A call whose arguments are checked and laid out once; ``run()`` enqueues it on the current stream.
+
+    The tensors given are kept and read (or written) by every ``run()``."""
+
+    def _enqueue(self, fn, where, *args):
+        # what a call does on every run: the device made current, the library's one call
+        if torch.cuda.current_device() == self.device.index:
+            rc = fn(*args, self.flags, torch._C._cuda_getCurrentRawStream(self.device.index))
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, self.flags, torch._C._cuda_getCurrentRawStream(self.device.index))
+        if rc != QG_OK:
+            raise QGError(rc, where)
+
+
+class KV8Cache:
+    """A paged 8-bit key-value cache (``qg_kv8_cache``).
+
+    ``codes``: int8 or float8_e4m3fn [2][n_pages][n_kv_heads][page_size][head_dim], keys then values;
+    ``scales``: fp32 [2][n_pages][n_kv_heads][page_size // scale_block]; ``page_table``: int32
+    [batch][max_pages].  All on one CUDA device, contiguous.  The page table may be rewritten in place
+    between calls (a page id is read when a call runs)."""
+
+    def __init__(self, codes, scales, page_table, scale_block: int = 16):
+        _need(codes, "codes", tuple(_FORMATS))
+        dev = codes.device
+        _need(scales, "scales", _F32, dev)
+        _need(page_table, "page_table", _I32, dev)
+        if codes.dim() != 5 or codes.shape[0] != 2:
+            raise ValueError("codes must be [2][n_pages][n_kv_heads][page_size][head_dim]")
+        _, pages, heads, page, d = codes.shape
+        if scale_block < 1 or tuple(scales.shape) != (2, pages, heads, page // scale_block):
+            raise ValueError("scales must be [2][n_pages][n_kv_heads][page_size // scale_block]")
+        if page_table.dim() != 2:
+            raise ValueError("page_table must be [batch][max_pages]")
+        self.codes, self.scales, self.page_table, self.scale_block = codes, scales, page_table, scale_block
+        self.device, self.n_kv_heads, self.head_dim = dev, heads, d
+        self.batch, self.max_pages = page_table.shape
+        self.struct = KV8CacheStruct(codes[0].data_ptr(), codes[1].data_ptr(), scales[0].data_ptr(),
+                                     scales[1].data_ptr(), page_table.data_ptr(), _FORMATS[codes.dtype], pages, heads,
+                                     d, page, scale_block, self.batch, self.max_pages)
+        self.ref = ctypes.cast(ctypes.pointer(self.struct), ctypes.c_void_p)
+
+    @classmethod
+    def empty(cls, n_pages, n_kv_heads, head_dim, batch, max_pages, page_size: int = 64, scale_block: int = 16,
+              dtype=torch.int8, device="cuda"):
+        """An empty cache; its page table starts at -1 (no page)."""
+        codes = torch.zeros((2, n_pages, n_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device).view(dtype)
+        scales = torch.zeros((2, n_pages, n_kv_heads, page_size // scale_block), dtype=torch.float32, device=device)
+        table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
+        return cls(codes, scales, table, scale_block)
+
+    def values(self):
+        """The fp32 values that the codes stand for, in the codes' shape (keys then values)."""
+        c = self.codes if self.codes.dtype == torch.int8 else self.codes.float()
+        v = c.unflatten(3, (-1, self.scale_block)) * self.scales[..., None, None]
+        return v.flatten(3, 4)
+
+    def _sequences(self, tokens, kv_len, cu_tokens):
+        _need(kv_len, "kv_len", _I32, self.device)
+        if kv_len.numel() != self.batch:
+            raise ValueError("kv_len must hold one length per sequence of the page table")
+        if cu_tokens is not None:
+            _need(cu_tokens, "cu_tokens", _I32, self.device)
+            if cu_tokens.numel() != self.batch + 1:
+                raise ValueError("cu_tokens must hold batch + 1 offsets")
+        elif tokens != self.batch:
+            raise ValueError("without cu_tokens there is one token per sequence")
+
+
+class KV8Append(_Plan):
+    """New keys and values [tokens][n_kv_heads][head_dim], rotated by position, into a :class:`KV8Cache`
+    (``kv8_rope_append``); with ``q`` [tokens][heads][head_dim] the queries rotated into ``q_out`` as well.
+
+    ``kv_len``: int32 [batch], the lengths WITH these tokens; ``cu_tokens``: int32 [batch+1] or None (one
+    token per sequence); ``cos``/``sin``: fp32 [n_pos][rot_dim/2] or None (no rotation); ``positions``:
+    int32 [tokens], rows of those tables (default: the cache positions); ``rope_style``: "half" or
+    "interleaved"."""
+
+    def __init__(self, cache, k, v, kv_len, cu_tokens=None, cos=None, sin=None, positions=None,
+                 rope_style: str = "half", q=None, q_out=None, flags: int = 0):
+        dev, d = cache.device, cache.head_dim
+        _need_rows(k, "k", cache.n_kv_heads, d, dev)
+        _need_rows(v, "v", cache.n_kv_heads, d, dev, k.dtype)
+        tokens = k.shape[0]
+        if v.shape[0] != tokens:
+            raise ValueError("k and v hold different numbers of tokens")
+        cache._sequences(tokens, kv_len, cu_tokens)
+        if (cos is None) != (sin is None):
+            raise ValueError("cos and sin come together")
+        rot = n_pos = 0
+        if cos is not None:
+            _need(cos, "cos", _F32, dev)
+            _need(sin, "sin", _F32, dev)
+            if cos.dim() != 2 or cos.shape != sin.shape:
+                raise ValueError("cos and sin must be [n_pos][rot_dim / 2]")
+            n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+        if positions is not None:
+            _need(positions, "positions", _I32, dev)
+            if positions.numel() != tokens:
+                raise ValueError("positions must hold one position per token")
+        if rope_style not in ("half", "interleaved"):
+            raise ValueError("rope_style is 'half' or 'interleaved'")
+        if q is not None:
+            _need_rows(q, "q", None, d, dev, k.dtype)
+            if q.shape[0] != tokens:
+                raise ValueError("q and k hold different numbers of tokens")
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+            _need_rows(q_out, "q_out", q.shape[1], d, dev, q.dtype)
+            if q_out.shape[0] != tokens:
+                raise ValueError("q and q_out hold different numbers of tokens")
+        elif q_out is not None:
+            raise ValueError("q_out without q")
+        self.device, self.flags, self.q_out = dev, flags, q_out
+        self.keep = (cache, k, v, kv_len, cu_tokens, cos, sin, positions, q)
+        p = [None if t is None else t.data_ptr() for t in (k, v, q, q_out, cos, sin, positions, kv_len, cu_tokens)]
+        s = [0 if t is None else _row_stride(t) for t in (k, v, q, q_out)]
+        self.args = KV8AppendArgs(*p, *s, tokens, 0 if q is None else q.shape[1], _DTYPES[k.dtype], rot,
+                                  QG_ROPE_HALF if rope_style == "half" else QG_ROPE_INTERLEAVED, n_pos)
+        self.refs = (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p))
+        self.fn = lib().kv8_rope_append
+
+    def run(self):
+        self._enqueue(self.fn, "kv8_rope_append", *self.refs)
+        return self.q_out
+
+
+def kv8_rope_append(cache, k, v, kv_len, cu_tokens=None, cos=None, sin=None, positions=None,
+                    rope_style: str = "half", q=None, q_out=None, flags: int = 0):
+    """One-shot :class:`KV8Append` call; returns the rotated queries (None without ``q``)."""
+    return KV8Append(cache, k, v, kv_len, cu_tokens, cos, sin, positions, rope_style, q, q_out, flags).run()
+
+
+def kv8_workspace(head_dim, device) -> torch.Tensor:
+    """A zero-filled workspace for :func:`kv8_attention` (reusable; calls leave its control words zero)."""
+    return torch.zeros(int(lib().kv8_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
+
+
+class KV8Attention(_Plan):
+    """Causal attention of ``q`` [tokens][heads][head_dim] over a :class:`KV8Cache` that already holds these
+    tokens' keys and values (``kv8_attention``).
+
+    ``kv_len``, ``cu_tokens`` as for :class:`KV8Append`; ``scale`` defaults to head_dim ** -0.5; ``window`` > 0
+    limits a token to its last ``window`` positions (its own included); ``softcap`` > 0 caps the scores;
+    ``lse``: fp32 [tokens][heads] that receives the log-sum-exp of the scores."""
+
+    def __init__(self, cache, q, kv_len, cu_tokens=None, out=None, scale=None, window: int = 0, softcap: float = 0.0,
+                 lse=None, ws=None, flags: int = 0):
+        dev, d = cache.device, cache.head_dim
+        _need_rows(q, "q", None, d, dev)
+        tokens, heads = q.shape[0], q.shape[1]
+        cache._sequences(tokens, kv_len, cu_tokens)
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev) if out is None else out
+        _need_rows(out, "out", heads, d, dev, q.dtype)
+        if out.shape[0] != tokens:
+            raise ValueError("q and out hold different numbers of tokens")
+        if lse is not None:
+            _need(lse, "lse", _F32, dev)
+            if lse.numel() != tokens * heads:
+                raise ValueError("lse must be [tokens][heads]")
+        ws = kv8_workspace(d, dev) if ws is None else ws
+        _need(ws, "ws", None, dev)
+        self.device, self.flags, self.out = dev, flags, out
+        self.keep = (cache, q, kv_len, cu_tokens, lse, ws)
+        p = [None if t is None else t.data_ptr() for t in (q, out, lse, kv_len, cu_tokens)]
+        self.args = KV8AttentionArgs(*p, _row_stride(q), _row_stride(out), tokens, heads, _DTYPES[q.dtype],
+                                     int(window), d ** -0.5 if scale is None else float(scale), float(softcap))
+        self.refs = (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p), ws.data_ptr(),
+                     ws.numel() * ws.element_size())
+        self.fn = lib().kv8_attention
+
+    def run(self):
+        self._enqueue(self.fn, "kv8_attention", *self.refs)
+        return self.out
+
+
+def kv8_attention(cache, q, kv_len, cu_tokens=None, out=None, scale=None, window: int = 0, softcap: float = 0.0,
+                  lse=None, ws=None, flags: int = 0):
+    """One-shot :class:`KV8Attention` call; returns ``out``."""
+    return KV8Attention(cache, q, kv_len, cu_tokens, out, scale, window, softcap, lse, ws, flags).run()
+
+
+def _need_norm(t, name, shape, dtypes, device):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
+    if tuple(t.shape) != tuple(shape) or (t.numel() > 1 and t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} must be {list(shape)} with contiguous rows, got {list(t.shape)}")
+
+
+class NormGateResidual(_Plan):
+    """The norm after a block, its gate and residual scale, and the norm before the next block
+    (``rmsnorm_gate_residual``), over rows of n values:
+
+    ``h_out = (h + gate * rms(y) * (w_post + w_offset)) * res_scale``, ``z = rms(h_out) * (w_pre + w_offset)``.
+
+    ``y`` [rows][n] or None (no block: h is only scaled and normed); ``h`` [rows][n], fp32 or y's dtype;
+    ``w_post``/``w_pre`` [n] or None (no such norm; without ``w_pre`` there is no z); ``gate`` [n], [rows][n]
+    or None; ``h_out`` may be ``h``, True to allocate it, or None not to store it."""
+
+    def __init__(self, y, h, w_post=None, w_pre=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+                 w_offset: float = 0.0, h_out=True, z=None, flags: int = 0):
+        if not isinstance(h, torch.Tensor) or h.dim() != 2:
+            raise TypeError("h must be a [rows][n] torch.Tensor")
+        dev, (rows, n) = h.device, h.shape
+        src = y if y is not None else w_pre if w_pre is not None else h
+        dtype = src.dtype if isinstance(src, torch.Tensor) else None
+        _need_norm(h, "h", (rows, n), (torch.float32, dtype) if dtype in _DTYPES else tuple(_DTYPES), dev)
+        for t, nm, shape in ((y, "y", (rows, n)), (w_post, "w_post", (n,)), (w_pre, "w_pre", (n,))):
+            if t is not None:
+                _need_norm(t, nm, shape, (dtype,) if dtype in _DTYPES else tuple(_DTYPES), dev)
+        if gate is not None:
+            _need_norm(gate, "gate", (n,) if gate.dim() == 1 else (rows, n), (dtype,), dev)
+        if h_out is True:
+            h_out = torch.empty((rows, n), dtype=h.dtype, device=dev)
+        if h_out is not None:
+            _need_norm(h_out, "h_out", (rows, n), (h.dtype,), dev)
+        if z is None and w_pre is not None:
+            z = torch.empty((rows, n), dtype=dtype, device=dev)
+        if z is not None:
+            if w_pre is None:
+                raise ValueError("z without w_pre")
+            _need_norm(z, "z", (rows, n), (dtype,), dev)
+        self.device, self.flags, self.h_out, self.z = dev, flags, h_out, z
+        self.keep = (y, h, w_post, w_pre, gate)
+        p = [None if t is None else t.data_ptr() for t in (y, h, gate, w_post, w_pre, h_out, z)]
+        # an expanded tensor's row stride may be 0 or overlap: the library refuses it
+        s = [0 if t is None or t.dim() == 1 else _row_stride(t) for t in (y, h, gate, h_out, z)]
+        if gate is not None and gate.dim() == 2 and s[2] == 0:
+            raise ValueError("a gate for every row must have rows of its own; pass [n] for one gate")
+        self.args = NormArgs(*p, *s, rows, n, _DTYPES[dtype], _DTYPES[h.dtype], float(eps), float(w_offset),
+                             float(res_scale))
+        self.refs = (ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p),)
+        self.fn = lib().rmsnorm_gate_residual
+
+    def run(self):
+        self._enqueue(self.fn, "rmsnorm_gate_residual", *self.refs)
+        return self.h_out, self.z
+
+
+def rmsnorm_gate_residual(y, h, w_post=None, w_pre=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,
+                          w_offset: float = 0.0, h_out=True, z=None, flags: int = 0):
+    """One-shot :class:`NormGateResidual` call; returns (h_out, z)."""
+    return NormGateResidual(y, h, w_post, w_pre, gate, res_scale, eps, w_offset, h_out, z, flags).run()
 
 
 def qg_quantize_act(x):

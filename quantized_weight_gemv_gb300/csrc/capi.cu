@@ -1,4 +1,5 @@
 // C ABI of the library: argument validation, variant choice, launch.
+#include <cmath>
 #include <mutex>
 
 #include "qg_internal.h"
@@ -182,6 +183,40 @@ int check_grouped(int bits, const qg_gemv_desc* descs, int count, int* active) {
         if (!aligned16(d.x) || !aligned16(d.y)) return QG_ERR_ALIGNMENT;
         ++*active;
     }
+    return QG_OK;
+}
+
+static bool pow2_in(int v, int lo, int hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
+
+static int check_kv8_cache(const qg_kv8_cache* c) {
+    if (!c) return QG_ERR_INVALID_ARG;
+    if (c->format != QG_KV8_INT8 && c->format != QG_KV8_E4M3) return QG_ERR_UNSUPPORTED;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QG_ERR_UNSUPPORTED;
+    if (!pow2_in(c->page_size, 16, 256) || !pow2_in(c->scale_block, 16, 64)) return QG_ERR_UNSUPPORTED;
+    if (c->scale_block > c->page_size || c->n_pages < 1 || c->n_kv_heads < 1 || c->batch < 1 || c->max_pages < 1)
+        return QG_ERR_INVALID_ARG;
+    // positions are 32-bit
+    if (c->batch > QG_KV8_MAX_BATCH || (long long)c->max_pages * c->page_size > 0x40000000ll) return QG_ERR_UNSUPPORTED;
+    if (!c->k || !c->v || !c->k_scale || !c->v_scale || !c->page_table) return QG_ERR_INVALID_ARG;
+    if (!aligned16(c->k) || !aligned16(c->v)) return QG_ERR_ALIGNMENT;
+    return QG_OK;
+}
+
+static size_t dtype_size(int dtype) { return dtype == QG_DTYPE_F32 ? 4 : 2; }
+static bool known_dtype(int dtype) { return dtype == QG_DTYPE_F32 || dtype == QG_DTYPE_F16 || dtype == QG_DTYPE_BF16; }
+
+// rows [tokens][heads][head_dim] of dtype, `stride` values apart
+static int check_kv8_rows(const void* p, long long stride, int heads, int head_dim, int dtype) {
+    if (!p || stride < (long long)heads * head_dim) return QG_ERR_INVALID_ARG;
+    if (!aligned16(p) || (stride * (long long)dtype_size(dtype)) % 16 != 0) return QG_ERR_ALIGNMENT;
+    return QG_OK;
+}
+
+// the calls' common arrays: token counts and offsets
+static int check_kv8_tokens(const qg_kv8_cache* c, int tokens, const int32_t* kv_len, const int32_t* cu, int dtype) {
+    if (!known_dtype(dtype)) return QG_ERR_UNSUPPORTED;
+    if (tokens < 0 || (!cu && tokens != c->batch)) return QG_ERR_INVALID_ARG;
+    if (tokens > 0 && !kv_len) return QG_ERR_INVALID_ARG;
     return QG_OK;
 }
 
@@ -443,6 +478,78 @@ int qgemv_grouped(int bits, const qg_gemv_desc* descs, int count, void* ws, size
     rc = resolve(stream, flags, lc);
     if (rc != QG_OK) return rc;
     return launch_grouped(bits, descs, count, reinterpret_cast<unsigned char*>(ws), lc);
+}
+
+int kv8_rope_append(const qg_kv8_cache* cache, const qg_kv8_append_args* a, unsigned flags, void* stream) {
+    int rc = check_kv8_cache(cache);
+    if (rc != QG_OK) return rc;
+    if (!a) return QG_ERR_INVALID_ARG;
+    rc = check_kv8_tokens(cache, a->tokens, a->kv_len, a->cu_tokens, a->dtype);
+    if (rc != QG_OK) return rc;
+    if (!a->cos != !a->sin || !a->q != !a->q_out || (a->q && a->n_q_heads < 1)) return QG_ERR_INVALID_ARG;
+    if (a->cos) {
+        if (a->rope_style != QG_ROPE_HALF && a->rope_style != QG_ROPE_INTERLEAVED) return QG_ERR_UNSUPPORTED;
+        if (a->rot_dim < 0 || a->rot_dim > cache->head_dim || a->rot_dim % 8 != 0 || a->n_pos < 1)
+            return QG_ERR_INVALID_ARG;
+        if (!aligned16(a->cos) || !aligned16(a->sin)) return QG_ERR_ALIGNMENT;
+    }
+    if (a->tokens == 0) return QG_OK;
+    rc = check_kv8_rows(a->k, a->k_stride, cache->n_kv_heads, cache->head_dim, a->dtype);
+    if (rc == QG_OK) rc = check_kv8_rows(a->v, a->v_stride, cache->n_kv_heads, cache->head_dim, a->dtype);
+    if (rc == QG_OK && a->q) rc = check_kv8_rows(a->q, a->q_stride, a->n_q_heads, cache->head_dim, a->dtype);
+    if (rc == QG_OK && a->q) rc = check_kv8_rows(a->q_out, a->q_out_stride, a->n_q_heads, cache->head_dim, a->dtype);
+    if (rc != QG_OK) return rc;
+    LaunchCtx lc;
+    rc = resolve(stream, flags, lc);
+    if (rc != QG_OK) return rc;
+    return launch_kv8_append(*cache, *a, lc);
+}
+
+size_t kv8_attention_workspace_bytes(int head_dim) {
+    return head_dim == 64 || head_dim == 128 || head_dim == 256 ? kv8_ws_bytes(head_dim) : 0;
+}
+
+int kv8_attention(const qg_kv8_cache* cache, const qg_kv8_attention_args* a, void* ws, size_t ws_bytes,
+                  unsigned flags, void* stream) {
+    int rc = check_kv8_cache(cache);
+    if (rc != QG_OK) return rc;
+    if (!a) return QG_ERR_INVALID_ARG;
+    rc = check_kv8_tokens(cache, a->tokens, a->kv_len, a->cu_tokens, a->dtype);
+    if (rc != QG_OK) return rc;
+    if (a->n_q_heads < 1 || a->n_q_heads % cache->n_kv_heads != 0) return QG_ERR_INVALID_ARG;
+    if (!std::isfinite(a->scale) || !std::isfinite(a->softcap)) return QG_ERR_INVALID_ARG;
+    if (a->tokens == 0) return QG_OK;
+    rc = check_kv8_rows(a->q, a->q_stride, a->n_q_heads, cache->head_dim, a->dtype);
+    if (rc == QG_OK) rc = check_kv8_rows(a->out, a->out_stride, a->n_q_heads, cache->head_dim, a->dtype);
+    if (rc != QG_OK) return rc;
+    if (!ws || ws_bytes < kv8_ws_bytes(cache->head_dim)) return QG_ERR_WORKSPACE;
+    if (!aligned16(ws)) return QG_ERR_ALIGNMENT;
+    LaunchCtx lc;
+    rc = resolve(stream, flags, lc);
+    if (rc != QG_OK) return rc;
+    return launch_kv8_attention(*cache, *a, reinterpret_cast<unsigned char*>(ws), lc);
+}
+
+int rmsnorm_gate_residual(const qg_norm_args* a, unsigned flags, void* stream) {
+    if (!a) return QG_ERR_INVALID_ARG;
+    if (!known_dtype(a->dtype) || (a->res_dtype != QG_DTYPE_F32 && a->res_dtype != a->dtype)) return QG_ERR_UNSUPPORTED;
+    if (a->rows < 0 || a->n < 1 || a->n > QG_MAX_NORM_N) return QG_ERR_INVALID_ARG;
+    if (!(a->eps >= 0.0f) || !std::isfinite(a->w_offset) || !std::isfinite(a->res_scale)) return QG_ERR_INVALID_ARG;
+    if (a->rows == 0) return QG_OK;
+    if (!a->h || (!a->w_pre != !a->z) || (!a->h_out && !a->z)) return QG_ERR_INVALID_ARG;
+    if (!a->y && (a->gate || a->w_post)) return QG_ERR_INVALID_ARG;
+    if ((a->y && a->y_stride < a->n) || a->h_stride < a->n || (a->h_out && a->h_out_stride < a->n) ||
+        (a->z && a->z_stride < a->n) || (a->gate && a->gate_stride != 0 && a->gate_stride < a->n))
+        return QG_ERR_INVALID_ARG;
+    const uintptr_t t = dtype_size(a->dtype) - 1, r = dtype_size(a->res_dtype) - 1;
+    auto off = [](const void* p, uintptr_t mask) { return (reinterpret_cast<uintptr_t>(p) & mask) != 0; };
+    if (off(a->y, t) || off(a->gate, t) || off(a->w_post, t) || off(a->w_pre, t) || off(a->z, t) || off(a->h, r) ||
+        off(a->h_out, r))
+        return QG_ERR_ALIGNMENT;
+    LaunchCtx lc;
+    int rc = resolve(stream, flags, lc);
+    if (rc != QG_OK) return rc;
+    return launch_norm(*a, lc);
 }
 
 int qg_quantize_act(const float* x, int k, int batch, int8_t* xq, float* xs, int32_t* xsum, void* stream) {

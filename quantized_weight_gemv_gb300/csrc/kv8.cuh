@@ -1,0 +1,107 @@
+// Shared parts of the kernels over the paged 8-bit key-value cache (sm_103a).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "qg_internal.h"
+
+namespace qg {
+namespace kv8 {
+
+// The cache as the kernels see it; sizes that are powers of two as shifts.
+struct CacheView {
+    uint8_t* k;
+    uint8_t* v;
+    float* ks;
+    float* vs;
+    const int32_t* table;
+    int n_pages, hkv, max_pages, batch;
+    int page_log2, block_log2;
+};
+
+inline int ilog2(int v) {
+    int l = 0;
+    while ((1 << l) < v) ++l;
+    return l;
+}
+
+inline CacheView view_of(const qg_kv8_cache& c) {
+    return CacheView{static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.k_scale, c.v_scale, c.page_table,
+                     c.n_pages,                  c.n_kv_heads,               c.max_pages, c.batch,
+                     ilog2(c.page_size),         ilog2(c.scale_block)};
+}
+
+// index of token slot 0 of (page, head) in tokens; times head_dim it is a code index,
+// shifted by block_log2 a scale index
+__device__ __forceinline__ long long slot_base(const CacheView& c, int page, int head) {
+    return ((long long)page * c.hkv + head) << c.page_log2;
+}
+
+// ---------------------------------------------------------------- rows of fp32, binary16 or bfloat16
+// eight consecutive values from a 16-byte aligned address
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+__device__ __forceinline__ void unpack2(const __half*, uint32_t w, float& a, float& b) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    a = f.x, b = f.y;
+}
+__device__ __forceinline__ void unpack2(const __nv_bfloat16*, uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16), b = __uint_as_float(w & 0xffff0000u);
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+    const uint4 w = *reinterpret_cast<const uint4*>(p);
+    unpack2(p, w.x, x[0], x[1]);
+    unpack2(p, w.y, x[2], x[3]);
+    unpack2(p, w.z, x[4], x[5]);
+    unpack2(p, w.w, x[6], x[7]);
+}
+// four consecutive values (8-byte aligned for the 16-bit types)
+__device__ __forceinline__ void load4(const float* p, float* x) {
+    const float4 a = *reinterpret_cast<const float4*>(p);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, float* x) {
+    const uint2 w = *reinterpret_cast<const uint2*>(p);
+    unpack2(p, w.x, x[0], x[1]);
+    unpack2(p, w.y, x[2], x[3]);
+}
+
+__device__ __forceinline__ uint32_t pack2(const __half*, float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack2(const __nv_bfloat16*, float a, float b) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float* x) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(p, x[0], x[1]), pack2(p, x[2], x[3]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+    store4(p, x);
+    store4(p + 4, x + 4);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+    *reinterpret_cast<uint4*>(p) =
+        make_uint4(pack2(p, x[0], x[1]), pack2(p, x[2], x[3]), pack2(p, x[4], x[5]), pack2(p, x[6], x[7]));
+}
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float v, float& x) { x = v; }
+__device__ __forceinline__ void from_float(float v, __half& x) { x = __float2half_rn(v); }
+__device__ __forceinline__ void from_float(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
+
+}  // namespace kv8
+}  // namespace qg

@@ -1,0 +1,330 @@
+// kv8_rope_append: new keys (rotated) and values into the paged 8-bit cache, and the
+// rotated queries, in one launch.
+//
+// One CTA per (block of scale_block tokens, kv head, k or v) that the call touches: it
+// holds the block's new values in registers (at most 32 a thread), reduces their largest
+// magnitude, and writes the codes against the block's scale - one read of the inputs and
+// one write of the codes, nothing kept between.  A block that already holds tokens is
+// rewritten only when its scale grows, and only that block's bytes (scale_block x
+// head_dim).  The remaining CTAs rotate queries, eight values a thread.
+#include "kv8.cuh"
+
+namespace qg {
+namespace kv8 {
+
+struct AppendParams {
+    CacheView c;
+    const void* k;
+    const void* v;
+    const void* q;
+    void* q_out;
+    const float* cos;
+    const float* sin;
+    const int32_t* positions;
+    const int32_t* kv_len;
+    const int32_t* cu;
+    long long k_stride, v_stride, q_stride, q_out_stride;
+    int tokens, hq, rot, n_pos;
+    int kv_ctas;  // virtual blocks; the first kv_ctas * 2 * hkv CTAs are cache units
+    unsigned* err;
+};
+
+// Eight values of a head, as the two groups of four consecutive ones that a rotation needs
+// together.  Half style: slot j < rot/8 holds 4j.. and rot/2 + 4j..; every other slot (and
+// every slot of the interleaved style) holds 8j.. and 8j + 4...
+template <bool HALF>
+__device__ __forceinline__ void slot_places(int j, int rot, int& a, int& b) {
+    if (HALF && 8 * j < rot) {
+        a = 4 * j;
+        b = (rot >> 1) + 4 * j;
+    } else {
+        a = 8 * j;
+        b = 8 * j + 4;
+    }
+}
+
+// the slot's pairs rotated by row `cs`/`sn` of the tables: (x[i], x[i+4]) in the half style,
+// (x[2i], x[2i+1]) in the interleaved one; every product and sum rounded on its own
+template <bool HALF>
+__device__ __forceinline__ void rotate_slot(float (&x)[8], const float* cs, const float* sn, int j) {
+    const float4 c4 = *reinterpret_cast<const float4*>(cs + 4 * j), s4 = *reinterpret_cast<const float4*>(sn + 4 * j);
+    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float& a = x[HALF ? i : 2 * i];
+        float& b = x[HALF ? i + 4 : 2 * i + 1];
+        const float ra = __fsub_rn(__fmul_rn(a, c[i]), __fmul_rn(b, s[i]));
+        const float rb = __fadd_rn(__fmul_rn(b, c[i]), __fmul_rn(a, s[i]));
+        a = ra;
+        b = rb;
+    }
+}
+
+template <int FMT>
+__device__ __forceinline__ uint32_t to_code(float x, float s, float inv) {
+    if (x != x || s == 0.0f) return 0u;
+    if constexpr (FMT == QG_KV8_INT8) {
+        return (uint32_t)quant_code(x, s, inv) & 255u;
+    } else {
+        return (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(x, s), __NV_SATFINITE, __NV_E4M3);
+    }
+}
+
+// four codes moved from scale s0 to scale s1 (s1 > s0 >= 0)
+template <int FMT>
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, float s0, float s1) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = (w >> (8 * i)) & 255u;
+        uint32_t o;
+        if constexpr (FMT == QG_KV8_INT8) {
+            const int q = __float2int_rn(__fdiv_rn(__fmul_rn((float)(int8_t)b, s0), s1));
+            o = (uint32_t)max(-127, min(127, q)) & 255u;
+        } else {
+            const __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
+            const float x = __half2float(__half(h));
+            o = x == x ? (uint32_t)__nv_cvt_float_to_fp8(__fdiv_rn(__fmul_rn(x, s0), s1), __NV_SATFINITE, __NV_E4M3) : 0u;
+        }
+        r |= o << (8 * i);
+    }
+    return r;
+}
+
+// The table row of token t at cache position pos, or -1 where there is none (no rotation).
+__device__ __forceinline__ int table_row(const AppendParams& p, int t, int pos) {
+    const int r = p.positions ? p.positions[t] : pos;
+    if ((unsigned)r < (unsigned)p.n_pos) return r;
+    atomicOr(p.err, ERR_KV_RANGE);
+    return -1;
+}
+
+constexpr int SLOTS = 4;  // slots of eight values per thread: 32 values in registers
+
+template <int D, int FMT, typename T, bool HALF>
+__device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* red) {
+    const CacheView& c = p.c;
+    const int nt = blockDim.x, tid = threadIdx.x;
+    const bool is_v = unit & 1;
+    const int h = (unit >> 1) % c.hkv, vb = (unit >> 1) / c.hkv;
+    // The sequence and block: sequence b owns the virtual blocks from
+    // floor(cu[b] / block) + 2b on, at least as many as it can touch.
+    int b = vb, t0 = vb, n = 1, j = 0;
+    if (p.cu) {
+        int upto = 0;
+        for (int s = 0; s < c.batch; s += nt) {
+            const int i = s + tid;
+            const int hit = __syncthreads_count(i < c.batch && (p.cu[i] >> c.block_log2) + 2 * i <= vb);
+            upto += hit;
+            if (hit < nt) break;  // ascending: nothing further on
+        }
+        b = upto - 1;
+        if (b < 0) return;
+        t0 = p.cu[b];
+        n = p.cu[b + 1] - t0;
+        j = vb - ((t0 >> c.block_log2) + 2 * b);
+        if (n <= 0 || t0 < 0 || t0 + n > p.tokens) {
+            if (tid == 0 && (n < 0 || (n > 0 && (t0 < 0 || t0 + n > p.tokens)))) atomicOr(p.err, ERR_KV_RANGE);
+            return;
+        }
+    }
+    const int len = p.kv_len[b], first = len - n;
+    const int block = 1 << c.block_log2;
+    const long long capacity = (long long)c.max_pages << c.page_log2;
+    if (first < 0 || len > capacity) {
+        if (tid == 0) atomicOr(p.err, ERR_KV_RANGE);
+        return;
+    }
+    const int start = ((first >> c.block_log2) + j) << c.block_log2;
+    if (start >= len) return;
+    const int lo = max(start, first), hi = min(start + block, len);
+    const int page = p.c.table[(long long)b * c.max_pages + (start >> c.page_log2)];
+    if ((unsigned)page >= (unsigned)c.n_pages) {
+        if (tid == 0) atomicOr(p.err, ERR_KV_RANGE);
+        return;
+    }
+    const long long slot = slot_base(c, page, h) + (start & ((1 << c.page_log2) - 1));
+    float* scale_at = (is_v ? c.vs : c.ks) + (slot >> c.block_log2);
+    uint8_t* codes = (is_v ? c.v : c.k) + slot * D;
+
+    constexpr int SPT = D / 8;  // slots per token
+    const T* src = reinterpret_cast<const T*>(is_v ? p.v : p.k);
+    const long long stride = is_v ? p.v_stride : p.k_stride;
+    const int rot = is_v ? 0 : p.rot;
+    float x[SLOTS][8];
+    float a = 0.0f;
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+        const int it = tid + i * nt;
+        const int pos = lo + it / SPT, sl = it % SPT;
+        if (pos >= hi) break;
+        const int t = t0 + pos - first;
+        int at, bt;
+        slot_places<HALF>(sl, rot, at, bt);
+        const T* row = src + t * stride + h * D;
+        load4(row + at, x[i]);
+        load4(row + bt, x[i] + 4);
+        if (8 * sl < rot) {
+            const int r = table_row(p, t, pos);
+            if (r >= 0)
+                rotate_slot<HALF>(x[i], p.cos + (long long)r * (rot >> 1), p.sin + (long long)r * (rot >> 1), sl);
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float m = fabsf(x[i][e]);
+            if (m < INFINITY) a = fmaxf(a, m);
+        }
+    }
+    const float s_old = start >= first ? 0.0f : *scale_at;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if ((tid & 31) == 0) red[tid >> 5] = a;
+    __syncthreads();
+    a = red[0];
+    for (int w = 1; w < (nt >> 5); ++w) a = fmaxf(a, red[w]);
+    const float s_new = fmaxf(s_old, __fdiv_rn(a, FMT == QG_KV8_INT8 ? 127.0f : 448.0f));
+    const float inv = s_new > 0.0f ? __frcp_rn(s_new) : 0.0f;
+
+    if (start >= first || s_new > s_old) {  // the block's other slots: cleared, or moved to the new scale
+        const int vecs = block * (D / 16);
+        for (int i = tid; i < vecs; i += nt) {
+            const int pos = start + i / (D / 16);
+            if (pos >= lo && pos < hi) continue;
+            uint4* at = reinterpret_cast<uint4*>(codes) + i;
+            uint4 w = make_uint4(0u, 0u, 0u, 0u);
+            if (start < first) {
+                w = *at;
+                w.x = rescale4<FMT>(w.x, s_old, s_new);
+                w.y = rescale4<FMT>(w.y, s_old, s_new);
+                w.z = rescale4<FMT>(w.z, s_old, s_new);
+                w.w = rescale4<FMT>(w.w, s_old, s_new);
+            }
+            *at = w;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < SLOTS; ++i) {
+        const int it = tid + i * nt;
+        const int pos = lo + it / SPT, sl = it % SPT;
+        if (pos >= hi) break;
+        int at, bt;
+        slot_places<HALF>(sl, rot, at, bt);
+        uint32_t w[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            w[f] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[f] |= to_code<FMT>(x[i][4 * f + e], s_new, inv) << (8 * e);
+        }
+        uint8_t* row = codes + (pos - start) * D;
+        *reinterpret_cast<uint32_t*>(row + at) = w[0];
+        *reinterpret_cast<uint32_t*>(row + bt) = w[1];
+    }
+    if (tid == 0) *scale_at = s_new;  // after the barrier above: every thread has read the old one
+}
+
+template <int D, typename T, bool HALF>
+__device__ __forceinline__ void q_unit(const AppendParams& p, long long item) {
+    constexpr int SPT = D / 8;
+    const int sl = (int)(item % SPT);
+    const long long th = item / SPT;
+    const int t = (int)(th / p.hq), h = (int)(th % p.hq);
+    if (t >= p.tokens) return;
+    int at, bt;
+    slot_places<HALF>(sl, p.rot, at, bt);
+    const T* row = reinterpret_cast<const T*>(p.q) + t * p.q_stride + h * D;
+    T* out = reinterpret_cast<T*>(p.q_out) + t * p.q_out_stride + h * D;
+    float x[8];
+    load4(row + at, x);
+    load4(row + bt, x + 4);
+    if (8 * sl < p.rot) {
+        int r = -1;
+        if (p.positions) {
+            r = table_row(p, t, 0);
+        } else {
+            int b = t, end = t + 1;
+            if (p.cu) {  // the last sequence that starts at or before t
+                int lo = 0, hi = p.c.batch;
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (p.cu[mid] <= t)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+                b = lo;
+                end = p.cu[b + 1];
+            }
+            r = table_row(p, t, p.kv_len[b] - end + t);
+        }
+        if (r >= 0)
+            rotate_slot<HALF>(x, p.cos + (long long)r * (p.rot >> 1), p.sin + (long long)r * (p.rot >> 1), sl);
+    }
+    store4(out + at, x);
+    store4(out + bt, x + 4);
+}
+
+template <int D, int FMT, typename T, bool HALF>
+__global__ void append_kernel(const AppendParams p) {
+    __shared__ float red[32];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int units = p.kv_ctas * 2 * p.c.hkv;
+    if ((int)blockIdx.x < units)
+        kv_unit<D, FMT, T, HALF>(p, blockIdx.x, red);
+    else
+        q_unit<D, T, HALF>(p, (long long)(blockIdx.x - units) * blockDim.x + threadIdx.x);
+}
+
+template <int D, int FMT, typename T>
+static int launch_d(const AppendParams& p, bool half, const LaunchCtx& lc) {
+    // one thread per SLOTS slots of a whole block, two warps at least
+    const int nt = max(64, (D / 8 << p.c.block_log2) / SLOTS);
+    const long long units = (long long)p.kv_ctas * 2 * p.c.hkv;
+    const long long items = p.q ? (long long)p.tokens * p.hq * (D / 8) : 0;
+    const long long grid = units + (items + nt - 1) / nt;
+    if (grid > 0x7fffffffll) return QG_ERR_UNSUPPORTED;
+    return half ? launch_kernel(append_kernel<D, FMT, T, true>, dim3((unsigned)grid), dim3(nt), 0, lc, p)
+                : launch_kernel(append_kernel<D, FMT, T, false>, dim3((unsigned)grid), dim3(nt), 0, lc, p);
+}
+
+template <int FMT, typename T>
+static int launch_t(const AppendParams& p, int d, bool half, const LaunchCtx& lc) {
+    switch (d) {
+        case 64:
+            return launch_d<64, FMT, T>(p, half, lc);
+        case 128:
+            return launch_d<128, FMT, T>(p, half, lc);
+        default:
+            return launch_d<256, FMT, T>(p, half, lc);
+    }
+}
+
+}  // namespace kv8
+
+int launch_kv8_append(const qg_kv8_cache& c, const qg_kv8_append_args& a, const LaunchCtx& lc) {
+    using namespace kv8;
+    AppendParams p;
+    p.c = view_of(c);
+    p.k = a.k, p.v = a.v, p.q = a.q, p.q_out = a.q_out;
+    p.cos = a.cos, p.sin = a.sin, p.positions = a.positions;
+    p.kv_len = a.kv_len, p.cu = a.cu_tokens;
+    p.k_stride = a.k_stride, p.v_stride = a.v_stride, p.q_stride = a.q_stride, p.q_out_stride = a.q_out_stride;
+    p.tokens = a.tokens, p.hq = a.n_q_heads, p.rot = a.cos ? a.rot_dim : 0, p.n_pos = a.n_pos;
+    // a sequence of n tokens touches at most floor(n / block) + 2 blocks; without cu one each
+    p.kv_ctas = a.cu_tokens ? (a.tokens >> p.c.block_log2) + 2 * c.batch : c.batch;
+    p.err = lc.err;
+    const bool half = a.rope_style == QG_ROPE_HALF, i8 = c.format == QG_KV8_INT8;
+    const int d = c.head_dim;
+    switch (a.dtype) {
+        case QG_DTYPE_F32:
+            return i8 ? launch_t<QG_KV8_INT8, float>(p, d, half, lc) : launch_t<QG_KV8_E4M3, float>(p, d, half, lc);
+        case QG_DTYPE_F16:
+            return i8 ? launch_t<QG_KV8_INT8, __half>(p, d, half, lc) : launch_t<QG_KV8_E4M3, __half>(p, d, half, lc);
+        default:
+            return i8 ? launch_t<QG_KV8_INT8, __nv_bfloat16>(p, d, half, lc)
+                      : launch_t<QG_KV8_E4M3, __nv_bfloat16>(p, d, half, lc);
+    }
+}
+
+}  // namespace qg

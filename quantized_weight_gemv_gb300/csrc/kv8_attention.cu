@@ -1,0 +1,675 @@
+// kv8_attention: attention of a call's tokens over the paged 8-bit cache.
+//
+// Work: (sequence, kv head, tile of RT query rows) x tiles of 16*W cache tokens, one flat
+// list that the CTAs share out evenly on the device from kv_len and cu_tokens, so ragged
+// batches balance and nothing about the lengths has to be known on the host.  Each CTA
+// takes a contiguous run of the list; a row tile that falls into several CTAs leaves one
+// partial (running maximum, sum, weighted values) per CTA, and the CTA that arrives last
+// adds them up in order.  No CTA waits for another.
+//
+// Mathematics: scores are held in base 2 (x = l * log2 e).  A warp takes 16 cache tokens at
+// a time: S^T = K Q^T with the tokens as the 16 rows of mma.m16n8k16 and up to 8 query rows
+// (grouped heads x tokens) as its columns, p = 2^(x - m), O^T += V^T P^T.  The codes are
+// small integers or 8-bit floats, exact in binary16, so K and V enter the tensor cores
+// without rounding and the block's scale multiplies afterwards: onto the score for K, onto
+// p for V.  Queries are brought to [-1, 1] by a power of two per row; fp32 queries and
+// their weights enter as two binary16 pieces (22 bits), 16-bit ones as one.  p is kept
+// times 2^10 so that small weights stay above binary16's subnormals.
+// The maximum m is only a reference: it moves when a score leaves it by more than 2^4
+// (voted, no reduction), which leaves the steady state without shuffles.
+#include "kv8.cuh"
+
+namespace qg {
+namespace kv8 {
+
+constexpr int W = 8;            // warps per CTA
+constexpr int SUB = 16;         // cache tokens per warp step
+constexpr int MAX_CTAS = 320;   // CTAs that share out one call (workspace slots)
+constexpr float P_BITS = 10.0f; // p is held as 2^(x - m + P_BITS)
+constexpr float P_SLACK = 4.0f; // x may exceed m by this much before m moves
+
+struct AttnParams {
+    CacheView c;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* kv_len;
+    const int32_t* cu;
+    long long q_stride, out_stride;
+    int tokens, hq, group, dtype, window;
+    float scale, softcap;
+    unsigned* counter;  // [MAX_CTAS], zero between calls
+    float* part_ml;     // [2 * MAX_CTAS][rows][2]
+    float* part_o;      // [2 * MAX_CTAS][rows * D]
+    unsigned* err;
+};
+
+// ---------------------------------------------------------------- device helpers
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// the 8x8 matrix of 16-bit values held one row-pair per lane, transposed
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes (bytes of w) as binary16 pairs (b0, b1) and (b2, b3).  int8: code + 128 as the
+// low byte of the binary16 1024 + (code + 128), less 1152: exact.  e4m3: a conversion.
+template <int FMT>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& p01, uint32_t& p23) {
+    if constexpr (FMT == QG_KV8_INT8) {
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
+        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+        p01 = *reinterpret_cast<const uint32_t*>(&x);
+        p23 = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        asm("{.reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;}"
+            : "=r"(p01), "=r"(p23)
+            : "r"(w));
+    }
+}
+
+// ---------------------------------------------------------------- the shared work list
+// Sequence b has hkv * qt_b row tiles of nt_b token tiles each; ends[b] counts the units of
+// sequences 0..b.
+struct SeqInfo {
+    int t0, n, len;  // first token of the call, tokens of the call, tokens in the cache
+    int qt, nt;      // row tiles per kv head, token tiles per row tile
+};
+
+template <int RT>
+__device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
+    SeqInfo s;
+    s.t0 = p.cu ? p.cu[b] : b;
+    s.n = p.cu ? p.cu[b + 1] - s.t0 : 1;
+    s.len = p.kv_len[b];
+    if (s.t0 < 0 || s.n < 0 || s.t0 + (long long)s.n > p.tokens) {
+        atomicOr(p.err, ERR_KV_RANGE);
+        s.n = 0;
+    }
+    if (s.len > ((long long)p.c.max_pages << p.c.page_log2) || s.len < 0) {
+        atomicOr(p.err, ERR_KV_RANGE);
+        s.len = 0;
+    }
+    s.qt = (int)(((long long)s.n * p.group + RT - 1) / RT);
+    // the widest row tile: RT rows span at most (RT - 1) / group + 2 tokens
+    const int span = p.window > 0 ? min((long long)s.len, (long long)p.window + (RT - 1) / p.group + 1 + SUB) : s.len;
+    s.nt = max(1, (span + W * SUB - 1) / (W * SUB));
+    return s;
+}
+
+// what a CTA's merge needs in shared memory beside the row tile's own arrays
+template <int D, int NT>
+struct Shape {
+    static constexpr int RT = 8 * NT;                 // query rows per tile
+    static constexpr int QUADS = D * NT / 16;         // groups of four values (per lane) of a row tile's output
+    static constexpr size_t merge_bytes = (size_t)W * RT * D * 4;
+};
+
+// One quad of the output: lane (g, t) holds d..d+3 of one column of the row tile.
+template <int D>
+__device__ __forceinline__ void quad_place(int quad, int lane, int& n, int& col, int& d) {
+    // quad = (n * 2 + parity) * (D / 32) + q
+    const int q = quad % (D / 32), ni = quad / (D / 32);
+    n = ni >> 1;
+    col = 8 * n + 2 * (lane & 3) + (ni & 1);
+    if (D >= 128)
+        d = (q >> 2) * 128 + (lane >> 2) * 16 + (q & 3) * 4;
+    else
+        d = (lane >> 2) * 8 + q * 4;
+}
+
+template <int D, int FMT, int PIECES, int NT>
+__global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kernel(const AttnParams p) {
+    using S = Shape<D, NT>;
+    constexpr int RT = S::RT;
+    constexpr int KC = D / 64;                       // 16-byte K loads per token row and lane
+    constexpr int VC = D >= 128 ? D / 128 : 1;       // V loads per token row and lane
+    constexpr int VB = D >= 128 ? 16 : 8;            // their bytes
+    constexpr int MT = D / 16;                       // m-tiles of the output
+    extern __shared__ __align__(16) unsigned char smem[];
+    __shared__ uint2 qf[PIECES][NT][MT][32];         // query fragments, in the order the MMAs read them
+    __shared__ float row_factor[RT];                 // 2^e * scale (* log2 e, or / softcap)
+    __shared__ int row_hi[RT], row_lo[RT];           // visible positions row_lo .. row_hi
+    __shared__ float wm[W][RT], wl[W][RT], wv[W];    // per warp: reference, sum, value-scale reference
+    __shared__ float tile_m[RT], tile_l[RT];
+    __shared__ long long total_s;
+    __shared__ int last_s;
+    long long* ends = reinterpret_cast<long long*>(smem);  // before the first row tile, then kept past the merge area
+    float* merge = reinterpret_cast<float*>(smem + (((size_t)p.c.batch * 8 + 15) & ~(size_t)15));
+
+    const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // prefix sums of the sequences' units
+    {
+        __shared__ long long wsum[W];
+        long long carry = 0;
+        for (int s = 0; s < p.c.batch; s += W * 32) {
+            long long u = 0;
+            if (s + tid < p.c.batch) {
+                const SeqInfo si = seq_info<RT>(p, s + tid);
+                u = (long long)p.c.hkv * si.qt * si.nt;
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, u, o);
+                if (lane >= o) u += v;
+            }
+            if (lane == 31) wsum[w] = u;
+            __syncthreads();
+            long long base = carry;
+            for (int i = 0; i < W; ++i) {
+                if (i < w) base += wsum[i];
+                carry += wsum[i];
+            }
+            if (s + tid < p.c.batch) ends[s + tid] = base + u;
+            __syncthreads();
+        }
+        if (tid == 0) total_s = carry;
+        __syncthreads();
+    }
+    const long long total = total_s;
+    const long long ctas = min((long long)gridDim.x, total);
+    if (blockIdx.x >= ctas) return;
+    long long pos = total * blockIdx.x / ctas;
+    const long long end = total * (blockIdx.x + 1) / ctas;
+    const long long my_start = pos;
+
+    while (pos < end) {
+        // the sequence of this unit, its row tile and the run of token tiles taken here
+        int b = 0;
+        {
+            int hi = p.c.batch - 1;
+            while (b < hi) {
+                const int mid = (b + hi) >> 1;
+                if (ends[mid] > pos)
+                    hi = mid;
+                else
+                    b = mid + 1;
+            }
+        }
+        const SeqInfo si = seq_info<RT>(p, b);
+        const long long base = b ? ends[b - 1] : 0;
+        const int seg = (int)((pos - base) / si.nt), tile0 = (int)((pos - base) % si.nt);
+        const int count = (int)min((long long)(si.nt - tile0), end - pos);
+        const long long seg_start = pos - tile0;
+        const int h = seg / si.qt, qt = seg % si.qt;
+
+        // ---- the tile's queries
+        const int rows = min(RT, si.n * p.group - qt * RT);
+        __syncthreads();  // the previous row tile's shared arrays are no longer read
+        for (int col = w; col < RT; col += W) {
+            const int r = qt * RT + col;
+            const bool valid = col < rows;
+            const int i = valid ? r / p.group : 0, hh = h * p.group + (valid ? r % p.group : 0);
+            constexpr int PER = D / 32;  // values per lane, consecutive
+            float x[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] = 0.0f;
+            if (valid) {
+                const long long at = (si.t0 + i) * p.q_stride + (long long)hh * D + lane * PER;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    if constexpr (PIECES == 2)
+                        x[e] = reinterpret_cast<const float*>(p.q)[at + e];
+                    else
+                        x[e] = p.dtype == QG_DTYPE_F16 ? __half2float(reinterpret_cast<const __half*>(p.q)[at + e])
+                                                       : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.q)[at + e]);
+                }
+            }
+            float a = 0.0f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[e]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
+            const float down = ldexpf(1.0f, -ex);
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                // value d: k-step (d / 64) * 4 + d % 16 / 4, lane 4 (col % 8) + d % 64 / 16, register d % 4 / 2
+                const int d = lane * PER + e;
+                const int ks = (d >> 6) * 4 + ((d & 15) >> 2), ln = (col & 7) * 4 + ((d & 63) >> 4), rg = (d & 3) >> 1;
+                const float u = x[e] * down, v = x[e + 1] * down;
+                const __half2 hi2 = __floats2half2_rn(u, v);
+                reinterpret_cast<uint32_t*>(&qf[0][col >> 3][ks][ln])[rg] = *reinterpret_cast<const uint32_t*>(&hi2);
+                if constexpr (PIECES == 2)
+                    reinterpret_cast<uint32_t*>(&qf[PIECES - 1][col >> 3][ks][ln])[rg] =
+                        half2_bits(u - __low2float(hi2), v - __high2float(hi2));
+            }
+            if (lane == 0) {
+                const int at = si.len - si.n + i;
+                const bool ok = valid && at >= 0 && at < si.len;
+                row_hi[col] = ok ? at : -1;
+                row_lo[col] = p.window > 0 ? max(0, at - p.window + 1) : 0;
+                row_factor[col] = ldexpf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f, ex);
+            }
+        }
+        __syncthreads();
+
+        // ---- this warp's state
+        float o[MT][NT][4];
+        float mo[NT][2], l[NT][2], rf[NT][2];
+        int hi_c[NT][2], lo_c[NT][2];
+        int hi_min = 0x7fffffff, hi_max = -1, lo_min = 0x7fffffff, lo_max = 0;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 8 * n + 2 * t + i;
+                mo[n][i] = -1e30f;
+                l[n][i] = 0.0f;
+                rf[n][i] = row_factor[col];
+                hi_c[n][i] = row_hi[col];
+                lo_c[n][i] = row_lo[col];
+            }
+        for (int r = 0; r < rows; ++r) {
+            const int hi = row_hi[r], lo = row_lo[r];
+            hi_min = min(hi_min, hi);
+            if (hi < 0) continue;
+            hi_max = max(hi_max, hi);
+            lo_min = min(lo_min, lo);
+            lo_max = max(lo_max, lo);
+        }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][n][i] = 0.0f;
+        float vref = 0.0f, vref_inv = 0.0f;  // power of two that the value scales are relative to
+        const float cap2 = p.softcap * 1.44269504088896f;
+
+        // ---- cache tokens, 16 per step: steps first + w, + W, ... of this run's tiles
+        const int origin = hi_max < 0 ? 0 : lo_min & ~(SUB - 1);
+        const int last_tok = min(hi_max + 1, origin + (tile0 + count) * W * SUB);  // one past
+        int tok = origin + (tile0 * W + w) * SUB;
+        const int32_t* table = p.c.table + (long long)b * p.c.max_pages;
+        const int pmask = (1 << p.c.page_log2) - 1;
+
+        uint4 kr[2][KC];
+        uint32_t vr[4][VC][VB / 4];
+        float ks = 0.0f, vs = 0.0f;
+        // a page id out of range reads page 0 and its tokens count as hidden
+        auto page_of = [&](int tk) { return tk < last_tok ? table[tk >> p.c.page_log2] : 0; };
+        auto slot_of = [&](int page, int tk) {
+            return slot_base(p.c, (unsigned)page < (unsigned)p.c.n_pages ? page : 0, h) + (tk & pmask);
+        };
+        auto load_k = [&](long long slot) {
+            const uint8_t* at = p.c.k + (slot + g) * D + t * 16;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int c = 0; c < KC; ++c) kr[r][c] = ldg_stream16(at + r * 8 * D + c * 64);
+            ks = __ldg(p.c.ks + (slot >> p.c.block_log2));
+        };
+        auto load_v = [&](long long slot) {
+            const uint8_t* at = p.c.v + (slot + 2 * t) * D + g * VB;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int c = 0; c < VC; ++c) {
+                    const uint8_t* a = at + ((r & 1) + (r >> 1) * 8) * D + c * 128;
+                    if constexpr (VB == 16) {
+                        const uint4 q4 = ldg_stream16(a);
+                        vr[r][c][0] = q4.x, vr[r][c][1] = q4.y, vr[r][c][2] = q4.z, vr[r][c][3] = q4.w;
+                    } else {
+                        const uint2 q2 = ldg_stream8(a);
+                        vr[r][c][0] = q2.x, vr[r][c][1] = q2.y;
+                    }
+                }
+            vs = __ldg(p.c.vs + (slot >> p.c.block_log2));
+        };
+
+        int page = page_of(tok), page_next = page_of(tok + W * SUB);
+        if (tok < last_tok) {
+            const long long s = slot_of(page, tok);
+            load_k(s);
+            load_v(s);
+        }
+        while (tok < last_tok) {
+            const int next = tok + W * SUB;
+            const long long slot_next = slot_of(page_next, next);
+            bool bad = (unsigned)page >= (unsigned)p.c.n_pages;
+            if (bad && lane == 0) atomicOr(p.err, ERR_KV_RANGE);
+            // scores
+            float s[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < KC; ++c) {
+                const uint32_t* k0 = reinterpret_cast<const uint32_t*>(&kr[0][c]);
+                const uint32_t* k1 = reinterpret_cast<const uint32_t*>(&kr[1][c]);
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    uint32_t a[4];
+                    codes_to_half<FMT>(k0[u], a[0], a[2]);
+                    codes_to_half<FMT>(k1[u], a[1], a[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int pc = 0; pc < PIECES; ++pc) {
+                            const uint2 f = qf[pc][n][c * 4 + u][lane];
+                            mma16816(s[n], a, f.x, f.y);
+                        }
+                }
+            }
+            const float ks_now = ks, vs_now = vs;
+            if (next < last_tok) load_k(slot_next);
+
+            // base-2 scores, masked
+            bool over = !(vs_now * vref_inv <= 2.0f) || vref == 0.0f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[n][i] * (rf[n][i & 1] * ks_now);
+                    if (p.softcap > 0.0f) x = cap2 * tanhf(x);
+                    s[n][i] = x;
+                }
+            const bool edge = bad || tok + SUB - 1 > hi_min || tok < lo_max;
+            if (edge) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = tok + g + (i >> 1) * 8;
+                        if (bad || j > hi_c[n][i & 1] || j < lo_c[n][i & 1]) s[n][i] = -INFINITY;
+                    }
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) over |= s[n][i] > mo[n][i & 1] + (P_BITS + P_SLACK);
+            if (__any_sync(0xffffffffu, over)) {  // move the references
+                float vr_new = vref;
+                if (!(vs_now * vref_inv <= 2.0f) || vref == 0.0f)  // the power of two at or below the scale
+                    vr_new = vs_now > 0.0f && vs_now < INFINITY ? __uint_as_float(__float_as_uint(vs_now) & 0x7f800000u) : vref;
+                if (vr_new == 0.0f) vr_new = vref;
+                const float vf = vr_new > 0.0f ? vref / vr_new : 0.0f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        float m = fmaxf(s[n][i], s[n][i + 2]);
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                        const float to = fmaxf(mo[n][i], m - P_BITS);
+                        const float f = ex2(mo[n][i] - to);
+                        l[n][i] *= f;
+                        mo[n][i] = to;
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            o[mt][n][i] *= f * vf;
+                            o[mt][n][i + 2] *= f * vf;
+                        }
+                    }
+                vref = vr_new;
+                vref_inv = vref > 0.0f ? 1.0f / vref : 0.0f;
+            }
+            // weights
+            uint32_t pf[PIECES][NT][2];
+            const float u = vs_now * vref_inv;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ex2(s[n][2 * r] - mo[n][0]), p1 = ex2(s[n][2 * r + 1] - mo[n][1]);
+                    l[n][0] += p0;
+                    l[n][1] += p1;
+                    // a hidden token's weight is 0 whatever its block's scale holds
+                    const float a = p0 == 0.0f ? 0.0f : p0 * u, c = p1 == 0.0f ? 0.0f : p1 * u;
+                    const __half2 hi2 = __floats2half2_rn(a, c);
+                    pf[0][n][r] = transpose8x8(*reinterpret_cast<const uint32_t*>(&hi2));
+                    if constexpr (PIECES == 2)
+                        pf[PIECES - 1][n][r] = transpose8x8(half2_bits(a - __low2float(hi2), c - __high2float(hi2)));
+                }
+            // slots that no row sees may hold anything: an 8-bit NaN must not meet the zero weight
+            if (FMT == QG_KV8_E4M3 && (tok + SUB - 1 > hi_max || tok < lo_min)) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int j = tok + 2 * t + (r & 1) + (r >> 1) * 8;
+                    if (j > hi_max || j < lo_min)
+#pragma unroll
+                        for (int c = 0; c < VC; ++c)
+#pragma unroll
+                            for (int e = 0; e < VB / 4; ++e) vr[r][c][e] = 0u;
+                }
+            }
+            // weighted values
+#pragma unroll
+            for (int c = 0; c < VC; ++c)
+#pragma unroll
+                for (int e = 0; e < VB / 4; ++e)
+#pragma unroll
+                    for (int f = 0; f < 2; ++f) {  // bytes 2f, 2f + 1 of the word: rows g and g + 8 of one m-tile
+                        uint32_t a[4];
+                        const uint32_t sel = f ? 0x7362 : 0x5140;
+                        codes_to_half<FMT>(__byte_perm(vr[0][c][e], vr[1][c][e], sel), a[0], a[1]);
+                        codes_to_half<FMT>(__byte_perm(vr[2][c][e], vr[3][c][e], sel), a[2], a[3]);
+                        const int mt = (c * (VB / 4) + e) * 2 + f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int pc = 0; pc < PIECES; ++pc) mma16816(o[mt][n], a, pf[pc][n][0], pf[pc][n][1]);
+                    }
+            if (next < last_tok) load_v(slot_next);
+            tok = next;
+            page = page_next;
+            page_next = page_of(tok + W * SUB);
+        }
+
+        // ---- the warps' shares of the row tile, added in shared memory
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+#pragma unroll
+                for (int d = 4; d < 32; d <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], d);
+                if (g == 0) {
+                    wm[w][8 * n + 2 * t + i] = mo[n][i];
+                    wl[w][8 * n + 2 * t + i] = l[n][i];
+                }
+            }
+        if (lane == 0) wv[w] = vref;
+        float4* mine = reinterpret_cast<float4*>(merge) + (size_t)w * S::QUADS * 32;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q)
+                    mine[((n * 2 + i) * (D / 32) + q) * 32 + lane] =
+                        make_float4(o[2 * q][n][i], o[2 * q][n][i + 2], o[2 * q + 1][n][i], o[2 * q + 1][n][i + 2]);
+        __syncthreads();
+        if (tid < RT) {
+            float m = wm[0][tid], sum = 0.0f;
+            for (int i = 1; i < W; ++i) m = fmaxf(m, wm[i][tid]);
+            for (int i = 0; i < W; ++i) {
+                const float f = ex2(wm[i][tid] - m);
+                sum += wl[i][tid] * f;
+                wm[i][tid] = f * wv[i];  // now the factor of warp i's values
+            }
+            tile_m[tid] = m;
+            tile_l[tid] = sum;
+        }
+        __syncthreads();
+
+        const bool whole = count == si.nt;
+        // a run that continues the previous CTA's row tile goes to its first slot, one that
+        // the next CTA continues to its second
+        const int slot_id = 2 * blockIdx.x + (seg_start >= my_start ? 1 : 0);
+        auto write_row = [&](int quad, float4 v) {
+            int n, col, d;
+            quad_place<D>(quad, lane, n, col, d);
+            if (col >= rows) return;
+            const float sum = tile_l[col];
+            const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+            const int r = qt * RT + col;
+            const long long at = (long long)(si.t0 + r / p.group) * p.out_stride + (long long)(h * p.group + r % p.group) * D + d;
+            const float x[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
+            if constexpr (PIECES == 2)
+                store4(reinterpret_cast<float*>(p.out) + at, x);
+            else if (p.dtype == QG_DTYPE_F16)
+                store4(reinterpret_cast<__half*>(p.out) + at, x);
+            else
+                store4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, x);
+        };
+        auto write_lse = [&]() {
+            if (p.lse && tid < rows) {
+                const int r = qt * RT + tid;
+                const float sum = tile_l[tid];
+                p.lse[(long long)(si.t0 + r / p.group) * p.hq + h * p.group + r % p.group] =
+                    sum == 0.0f ? -INFINITY : (tile_m[tid] + log2f(sum)) * 0.693147180559945f;
+            }
+        };
+        for (int quad = w; quad < S::QUADS; quad += W) {
+            int n, col, d;
+            quad_place<D>(quad, lane, n, col, d);
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const float4 v = reinterpret_cast<const float4*>(merge)[((size_t)i * S::QUADS + quad) * 32 + lane];
+                const float f = wm[i][col];
+                acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+            }
+            if (whole)
+                write_row(quad, acc);
+            else
+                reinterpret_cast<float4*>(p.part_o)[((size_t)slot_id * S::QUADS + quad) * 32 + lane] = acc;
+        }
+        if (whole) {
+            write_lse();
+        } else {
+            if (tid < RT) {
+                p.part_ml[((size_t)slot_id * RT + tid) * 2] = tile_m[tid];
+                p.part_ml[((size_t)slot_id * RT + tid) * 2 + 1] = tile_l[tid];
+            }
+            // the CTAs of this row tile: those that hold its first and its last unit
+            const int c0 = (int)(((seg_start + 1) * ctas - 1) / total);
+            const int c1 = (int)(((seg_start + si.nt) * ctas - 1) / total);
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                unsigned prev;
+                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(p.counter + c0) : "memory");
+                last_s = prev == (unsigned)(c1 - c0);
+                if (last_s) p.counter[c0] = 0u;  // every CTA of the row tile has arrived
+            }
+            __syncthreads();
+            if (last_s) {
+                __threadfence();
+                auto slot_of_cta = [&](int c) {
+                    return (size_t)(2 * c + (c == c0 ? 1 : 0));  // only c0 begins the row tile
+                };
+                if (tid < RT) {
+                    float m = -1e30f;
+                    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(p.part_ml + (slot_of_cta(c) * RT + tid) * 2));
+                    float sum = 0.0f;
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* at = p.part_ml + (slot_of_cta(c) * RT + tid) * 2;
+                        sum += __ldcg(at + 1) * ex2(__ldcg(at) - m);
+                    }
+                    tile_m[tid] = m;
+                    tile_l[tid] = sum;
+                }
+                __syncthreads();
+                for (int quad = w; quad < S::QUADS; quad += W) {
+                    int n, col, d;
+                    quad_place<D>(quad, lane, n, col, d);
+                    const float m = tile_m[col];
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int c = c0; c <= c1; ++c) {
+                        const size_t sl = slot_of_cta(c);
+                        const float f = ex2(__ldcg(p.part_ml + (sl * RT + col) * 2) - m);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (sl * S::QUADS + quad) * 32 + lane);
+                        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+                    }
+                    write_row(quad, acc);
+                }
+                write_lse();
+            }
+        }
+        pos += count;
+    }
+}
+
+template <int D, int FMT, int PIECES, int NT>
+static int launch_nt(AttnParams& p, unsigned char* ws, const LaunchCtx& lc) {
+    using S = Shape<D, NT>;
+    p.counter = reinterpret_cast<unsigned*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + QG_KV8_CTL_BYTES);
+    p.part_o = p.part_ml + (size_t)2 * MAX_CTAS * S::RT * 2;
+    const size_t smem = (((size_t)p.c.batch * 8 + 15) & ~(size_t)15) + S::merge_bytes;
+    const void* kernel = reinterpret_cast<const void*>(attention_kernel<D, FMT, PIECES, NT>);
+    const int rc = ensure_smem_attr(kernel, smem, lc);
+    if (rc != QG_OK) return rc;
+    // no more CTAs than resident at once, nor than there can be units
+    const long long tiles = (((long long)p.c.max_pages << p.c.page_log2) + W * SUB - 1) / (W * SUB);
+    const long long qt = (long long)p.tokens * p.group / S::RT + p.c.batch;
+    const long long grid = min(min((long long)MAX_CTAS, (long long)lc.sm_count * (D * NT <= 128 ? 2 : 1)),
+                               p.c.hkv * qt * tiles);
+    return launch_kernel(attention_kernel<D, FMT, PIECES, NT>, dim3((unsigned)grid), dim3(W * 32), smem, lc, p);
+}
+
+template <int D, int FMT, int PIECES>
+static int launch_rows(AttnParams& p, unsigned char* ws, const LaunchCtx& lc) {
+    // query rows per kv head and sequence, on average
+    const long long rows = (long long)p.tokens * p.group / p.c.batch;
+    return rows <= 8 ? launch_nt<D, FMT, PIECES, 1>(p, ws, lc) : launch_nt<D, FMT, PIECES, 2>(p, ws, lc);
+}
+
+template <int FMT, int PIECES>
+static int launch_d(AttnParams& p, int d, unsigned char* ws, const LaunchCtx& lc) {
+    switch (d) {
+        case 64:
+            return launch_rows<64, FMT, PIECES>(p, ws, lc);
+        case 128:
+            return launch_rows<128, FMT, PIECES>(p, ws, lc);
+        default:
+            return launch_rows<256, FMT, PIECES>(p, ws, lc);
+    }
+}
+
+}  // namespace kv8
+
+size_t kv8_ws_bytes(int d) {
+    using namespace kv8;
+    return QG_KV8_CTL_BYTES + (size_t)2 * MAX_CTAS * 16 * (d + 2) * 4;
+}
+
+int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, unsigned char* ws, const LaunchCtx& lc) {
+    using namespace kv8;
+    AttnParams p = {};
+    p.c = view_of(c);
+    p.q = a.q, p.out = a.out, p.lse = a.lse, p.kv_len = a.kv_len, p.cu = a.cu_tokens;
+    p.q_stride = a.q_stride, p.out_stride = a.out_stride;
+    p.tokens = a.tokens, p.hq = a.n_q_heads, p.group = a.n_q_heads / c.n_kv_heads, p.dtype = a.dtype;
+    p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
+    p.err = lc.err;
+    const bool f32 = a.dtype == QG_DTYPE_F32;
+    if (c.format == QG_KV8_INT8)
+        return f32 ? launch_d<QG_KV8_INT8, 2>(p, c.head_dim, ws, lc) : launch_d<QG_KV8_INT8, 1>(p, c.head_dim, ws, lc);
+    return f32 ? launch_d<QG_KV8_E4M3, 2>(p, c.head_dim, ws, lc) : launch_d<QG_KV8_E4M3, 1>(p, c.head_dim, ws, lc);
+}
+
+}  // namespace qg

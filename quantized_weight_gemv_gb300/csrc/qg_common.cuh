@@ -11,9 +11,17 @@ namespace qg {
 
 // Codes OR-ed into the device error word (its address is a kernel parameter) by a
 // kernel whose bounded wait ran out (1, 2, 4, 8), or by a CTA of the persistent chain
-// that stopped on the chain's abort word (16).  Host side: qg_device_error() reads and
+// that stopped on the chain's abort word (16), or by a cache kernel that met a page id or
+// position out of range and skipped it (32).  Host side: qg_device_error() reads and
 // clears it.
-enum : unsigned { ERR_WAIT_FULL = 1u, ERR_WAIT_EMPTY = 2u, ERR_WAIT_DRAIN = 4u, ERR_WAIT_GRID = 8u, ERR_ABORTED = 16u };
+enum : unsigned {
+    ERR_WAIT_FULL = 1u,
+    ERR_WAIT_EMPTY = 2u,
+    ERR_WAIT_DRAIN = 4u,
+    ERR_WAIT_GRID = 8u,
+    ERR_ABORTED = 16u,
+    ERR_KV_RANGE = 32u
+};
 
 constexpr int WARP = 32;
 // 1 s: far beyond any legitimate wait of these kernels, short enough to keep the context alive.

@@ -146,6 +146,10 @@ int launch_chain(int bits, const qg_gemv_desc* descs, int count, const int* phas
                  unsigned char* ws, const LaunchCtx& lc);
 int launch_select(const float* logits, int n, const int32_t* allowed, int n_allowed, int32_t* token, float* logprob,
                   SelectWorkspace* ws, const LaunchCtx& lc);
+int launch_kv8_append(const qg_kv8_cache& c, const qg_kv8_append_args& a, const LaunchCtx& lc);
+size_t kv8_ws_bytes(int head_dim);
+int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, unsigned char* ws, const LaunchCtx& lc);
+int launch_norm(const qg_norm_args& a, const LaunchCtx& lc);
 int launch_read_floor(const void* src, size_t bytes, uint32_t* out, const LaunchCtx& lc);
 int launch_quantize_act(const float* x, int k, int batch, int8_t* xq, float* xs, int32_t* xsum, const LaunchCtx& lc);
 int launch_blockdots(int bits, const uint8_t* lo, const uint8_t* hi, int n, int k, const int8_t* xq, int32_t* dots,

@@ -1,0 +1,144 @@
+"""rmsnorm_gate_residual on the GPU against the definition in 64 bits."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import quantized_weight_gemv_gb300 as qg
+from tests import _kv8 as K
+from tests._gpu import DEV
+
+pytestmark = pytest.mark.gpu
+
+F32, F16, BF16 = torch.float32, torch.float16, torch.bfloat16
+# fp32: a row's sum of squares goes through at most 32 adds in a thread and 10 levels of
+# reduction (42 * 2^-24 of the sum, half of that after the root), the reciprocal root and
+# four products another 2^-22: below 2^-19 of an output, h' adds one rounding of each term.
+# 16 bits: the output's own rounding.
+REL = {F32: 2.0 ** -19, F16: 2.0 ** -10, BF16: 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from quantized_weight_gemv_gb300 import build
+    build.build()
+    assert torch.cuda.is_available()
+
+
+def near(got, ref, dtype, size):
+    """|got - ref| within REL of the largest term that went into it."""
+    err = np.abs(got.double().cpu().numpy() - ref)
+    bound = REL[dtype] * np.maximum(np.abs(ref), size)
+    assert np.isfinite(got.double().cpu().numpy()).all()
+    assert (err <= bound).all(), f"off by {np.max(err / bound):.2f} of the bound"
+
+
+def check(rows, n, dtype, res, gate="none", post=True, pre=True, y=True, scale=0.75, offset=1.0, eps=1e-6, seed=0,
+          pad=0, shift=0, in_place=False):
+    rng = np.random.default_rng(seed + rows * n)
+
+    def make(shape, dt, gain=1.0):
+        """A tensor of `shape` inside a wider one: rows `pad` apart, the base `shift` values in."""
+        t = torch.from_numpy((gain * rng.standard_normal(shape)).astype(np.float32)).to(dt)
+        if len(shape) == 1:
+            store = torch.zeros(shape[0] + shift, dtype=dt, device=DEV)
+            view = store[shift:]
+        else:
+            store = torch.zeros((shape[0], shape[1] + pad + shift), dtype=dt, device=DEV)
+            view = store[:, shift:shift + shape[1]]
+        view.copy_(t)
+        return view, t.double().numpy()
+
+    Y, y64 = make((rows, n), dtype) if y else (None, None)
+    H, h64 = make((rows, n), res, 5.0)
+    P, p64 = make((n,), dtype) if post and y else (None, None)
+    W, w64 = make((n,), dtype) if pre else (None, None)
+    G, g64 = (None, None) if gate == "none" or not y else make((n,) if gate == "vector" else (rows, n), dtype)
+    ref_h, ref_z = K.norm(y64, h64, p64, w64, g64, float(np.float32(scale)), float(np.float32(eps)), offset)
+    h_out, z = qg.rmsnorm_gate_residual(Y, H, P, W, gate=G, res_scale=scale, eps=eps, w_offset=offset,
+                                        h_out=H if in_place else True, z=Y if in_place and pre and y else None)
+    if not rows:
+        assert h_out.shape == (0, n)
+        return
+    u = 0.0 if not y else np.abs(ref_h / scale - h64)
+    near(h_out, ref_h, res, (np.abs(h64) + u) * scale)
+    if pre:
+        root = np.sqrt((ref_h ** 2).mean(-1, keepdims=True) + eps)
+        near(z, ref_z, dtype, (np.abs(h64) + u) * scale / root * np.abs(w64 + offset) * 2)
+    else:
+        assert z is None
+
+
+SIZES = [(1, 1), (1, 2048), (3, 64), (5, 255), (2, 256), (7, 1000), (4, 1024), (3, 1025), (2, 1531), (2, 8192), (1, 8200),
+         (2, 16384), (1, 32768), (1, 32767), (300, 96)]
+
+
+@pytest.mark.parametrize("types", [(F32, F32), (BF16, F32), (BF16, BF16), (F16, F32), (F16, F16)])
+@pytest.mark.parametrize("rows,n", SIZES)
+def test_sizes_and_types(rows, n, types):
+    check(rows, n, *types, gate="row" if rows % 2 else "vector")
+
+
+@pytest.mark.parametrize("gate,post,pre,y", [c for c in itertools.product(("none", "vector", "row"), (True, False),
+                                                                         (True, False), (True, False))])
+@pytest.mark.parametrize("n", [128, 2048, 4097])
+def test_parts(gate, post, pre, y, n):
+    check(3, n, F32, F32, gate=gate, post=post, pre=pre, y=y, offset=0.0, scale=1.0)
+
+
+@pytest.mark.parametrize("pad,shift", [(8, 0), (16, 8), (1, 0), (3, 5)])
+@pytest.mark.parametrize("n", [512, 2048, 777])
+def test_strides_and_alignment(pad, shift, n):
+    check(5, n, F32, F32, gate="row", pad=pad, shift=shift)
+    check(5, n, BF16, F32, gate="vector", pad=pad, shift=shift)
+
+
+@pytest.mark.parametrize("n", [200, 2048, 9001])
+def test_in_place(n):
+    check(6, n, F32, F32, gate="row", in_place=True)
+    check(6, n, BF16, BF16, in_place=True)
+
+
+def test_rows_of_zeros_and_no_rows():
+    z = torch.zeros(3, 320, device=DEV)
+    w = torch.ones(320, device=DEV)
+    h, out = qg.rmsnorm_gate_residual(z, z, w, w)
+    assert not h.any() and not out.any()
+    check(0, 64, F32, F32)
+
+
+def test_large_and_small_values():
+    """Squares near the fp32 range's ends still give finite norms; NaN stays in its row."""
+    h = torch.full((3, 512), 1e17, device=DEV)
+    y = torch.full((3, 512), 1e-15, device=DEV)
+    y[1, 7] = float("nan")
+    w = torch.ones(512, device=DEV)
+    out, z = qg.rmsnorm_gate_residual(y, h, w, w, eps=1e-30)
+    assert torch.isfinite(z[[0, 2]]).all() and torch.isnan(z[1]).all()
+    assert np.allclose(z[[0, 2]].cpu().numpy(), 1.0, atol=2e-6)
+
+
+def test_norm_in_a_graph_with_dependent_launch():
+    """Two norms of a layer captured on a side stream, the second reading what the first wrote."""
+    rng = np.random.default_rng(4)
+    t = lambda *shape: torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).to(DEV)  # noqa: E731
+    y, h, w1, w2, w3 = t(2, 2048), t(2, 2048), t(2048), t(2048), t(2048)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        a = qg.NormGateResidual(y, h, w1, w2, flags=qg.QG_FLAG_PDL)
+        b = qg.NormGateResidual(a.z, a.h_out, w2, w3, flags=qg.QG_FLAG_PDL)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            a.run()
+            b.run()
+        for step in range(2):
+            y.copy_(t(2, 2048))
+            g.replay()
+            side.synchronize()
+            d = lambda x: x.double().cpu().numpy()  # noqa: E731
+            h1, z1 = K.norm(d(y), d(h), d(w1), d(w2), None, 1.0, float(np.float32(1e-6)), 0.0)
+            h2, z2 = K.norm(z1, h1, d(w2), d(w3), None, 1.0, float(np.float32(1e-6)), 0.0)
+            assert np.abs(d(b.h_out) - h2).max() <= 2.0 ** -17 * np.abs(h2).max()
+            assert np.abs(d(b.z) - z2).max() <= 2.0 ** -17 * np.abs(z2).max()
