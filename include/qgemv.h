@@ -334,6 +334,9 @@ int qgemv_chain(int bits, const qg_gemv_desc* descs, int count, const int* phase
  * These arrays and the page table are read on the device.  A position or a page id out of
  * range there is skipped (its token is neither written nor attended to) and sets 32 in the
  * device error word (qg_device_error).
+ * These calls and rmsnorm_gate_residual touch no memory before the preceding work on the
+ * stream has finished, and are always launched as its programmatic dependents (QG_FLAG_PDL
+ * adds nothing).
  * Rows of a call: [tokens][heads][head_dim] of `dtype`, the heads of a token contiguous and
  * tokens `*_stride` values apart (a multiple of 16 bytes); bases on 16-byte boundaries.
  */
@@ -404,6 +407,13 @@ typedef struct qg_kv8_append_args {
 } qg_kv8_append_args;
 
 int kv8_rope_append(const qg_kv8_cache* cache, const qg_kv8_append_args* args, unsigned flags, void* stream);
+
+/*
+ * kv8_values: the fp32 values that the codes of the whole pool stand for (scale * code), keys
+ * to k_out and values to v_out, each device fp32 [n_pages][n_kv_heads][page_size][head_dim]
+ * on a 16-byte boundary, or NULL to leave one out.
+ */
+int kv8_values(const qg_kv8_cache* cache, float* k_out, float* v_out, unsigned flags, void* stream);
 
 /*
  * kv8_attention: causal attention of the call's tokens over the cache, which already holds

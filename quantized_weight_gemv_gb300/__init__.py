@@ -66,6 +66,7 @@ SIGNATURES = {
     "qg_chain_workspace_bytes": (_sz, [_vp, _i, _vp, _i]),
     "qgemv_chain": (_i, [_i, _vp, _i, _vp, _i, _vp, _sz, _u, _vp]),
     "kv8_rope_append": (_i, [_vp, _vp, _u, _vp]),
+    "kv8_values": (_i, [_vp, _vp, _vp, _u, _vp]),
     "kv8_attention_workspace_bytes": (_sz, [_i]),
     "kv8_attention": (_i, [_vp, _vp, _vp, _sz, _u, _vp]),
     "rmsnorm_gate_residual": (_i, [_vp, _u, _vp]),
@@ -482,20 +483,29 @@ def _row_stride(t):
     return t.stride(0) if t.shape[0] > 1 else math.prod(t.shape[1:])
 
 
+# the current device and its current stream, without the wrappers' per-call cost
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _Plan:
     """A call whose arguments are checked and laid out once; ``run()`` enqueues it on the current stream.
 
     The tensors given are kept and read (or written) by every ``run()``."""
 
-    def _enqueue(self, fn, where, *args):
-        # what a call does on every run: the device made current, the library's one call
-        if torch.cuda.current_device() == self.device.index:
-            rc = fn(*args, self.flags, torch._C._cuda_getCurrentRawStream(self.device.index))
-        else:
+    def _bind(self, device, fn, where, refs, result):
+        self.device, self._index, self._where = device, device.index, where
+        self._fn, self._refs, self._result = fn, refs, result
+
+    def run(self):
+        i = self._index
+        if _current_device() != i:
             with torch.cuda.device(self.device):
-                rc = fn(*args, self.flags, torch._C._cuda_getCurrentRawStream(self.device.index))
-        if rc != QG_OK:
-            raise QGError(rc, where)
+                return self.run()
+        rc = self._fn(*self._refs, _raw_stream(i))
+        if rc:
+            raise QGError(rc, self._where)
+        return self._result
 
 
 class KV8Cache:
@@ -525,6 +535,9 @@ class KV8Cache:
                                      scales[1].data_ptr(), page_table.data_ptr(), _FORMATS[codes.dtype], pages, heads,
                                      d, page, scale_block, self.batch, self.max_pages)
         self.ref = ctypes.cast(ctypes.pointer(self.struct), ctypes.c_void_p)
+        # what values() needs on every call
+        self._index, self._shape, self._v_offset = dev.index, codes.shape, codes.numel() * 2
+        self._values = lib().kv8_values
 
     @classmethod
     def empty(cls, n_pages, n_kv_heads, head_dim, batch, max_pages, page_size: int = 64, scale_block: int = 16,
@@ -535,11 +548,22 @@ class KV8Cache:
         table = torch.full((batch, max_pages), -1, dtype=torch.int32, device=device)
         return cls(codes, scales, table, scale_block)
 
-    def values(self):
+    def values(self, out=None):
         """The fp32 values that the codes stand for, in the codes' shape (keys then values)."""
-        c = self.codes if self.codes.dtype == torch.int8 else self.codes.float()
-        v = c.unflatten(3, (-1, self.scale_block)) * self.scales[..., None, None]
-        return v.flatten(3, 4)
+        if out is None:
+            out = self.scales.new_empty(self._shape)
+        else:
+            _need(out, "out", _F32, self.device)
+            if out.shape != self._shape:
+                raise ValueError("out must have the codes' shape")
+        if _current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.values(out)
+        at = out.data_ptr()
+        rc = self._values(self.ref, at, at + self._v_offset, 0, _raw_stream(self._index))
+        if rc:
+            raise QGError(rc, "kv8_values")
+        return out
 
     def _sequences(self, tokens, kv_len, cu_tokens):
         _need(kv_len, "kv_len", _I32, self.device)
@@ -596,18 +620,14 @@ class KV8Append(_Plan):
                 raise ValueError("q and q_out hold different numbers of tokens")
         elif q_out is not None:
             raise ValueError("q_out without q")
-        self.device, self.flags, self.q_out = dev, flags, q_out
+        self.q_out = q_out
         self.keep = (cache, k, v, kv_len, cu_tokens, cos, sin, positions, q)
         p = [None if t is None else t.data_ptr() for t in (k, v, q, q_out, cos, sin, positions, kv_len, cu_tokens)]
         s = [0 if t is None else _row_stride(t) for t in (k, v, q, q_out)]
         self.args = KV8AppendArgs(*p, *s, tokens, 0 if q is None else q.shape[1], _DTYPES[k.dtype], rot,
                                   QG_ROPE_HALF if rope_style == "half" else QG_ROPE_INTERLEAVED, n_pos)
-        self.refs = (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p))
-        self.fn = lib().kv8_rope_append
-
-    def run(self):
-        self._enqueue(self.fn, "kv8_rope_append", *self.refs)
-        return self.q_out
+        self._bind(dev, lib().kv8_rope_append, "kv8_rope_append",
+                   (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p), flags), q_out)
 
 
 def kv8_rope_append(cache, k, v, kv_len, cu_tokens=None, cos=None, sin=None, positions=None,
@@ -645,18 +665,14 @@ class KV8Attention(_Plan):
                 raise ValueError("lse must be [tokens][heads]")
         ws = kv8_workspace(d, dev) if ws is None else ws
         _need(ws, "ws", None, dev)
-        self.device, self.flags, self.out = dev, flags, out
+        self.out = out
         self.keep = (cache, q, kv_len, cu_tokens, lse, ws)
         p = [None if t is None else t.data_ptr() for t in (q, out, lse, kv_len, cu_tokens)]
         self.args = KV8AttentionArgs(*p, _row_stride(q), _row_stride(out), tokens, heads, _DTYPES[q.dtype],
                                      int(window), d ** -0.5 if scale is None else float(scale), float(softcap))
-        self.refs = (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p), ws.data_ptr(),
-                     ws.numel() * ws.element_size())
-        self.fn = lib().kv8_attention
-
-    def run(self):
-        self._enqueue(self.fn, "kv8_attention", *self.refs)
-        return self.out
+        self._bind(dev, lib().kv8_attention, "kv8_attention",
+                   (cache.ref, ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p), _ptr(ws),
+                    ws.numel() * ws.element_size(), flags), out)
 
 
 def kv8_attention(cache, q, kv_len, cu_tokens=None, out=None, scale=None, window: int = 0, softcap: float = 0.0,
@@ -711,7 +727,7 @@ class NormGateResidual(_Plan):
             if w_pre is None:
                 raise ValueError("z without w_pre")
             _need_norm(z, "z", (rows, n), (dtype,), dev)
-        self.device, self.flags, self.h_out, self.z = dev, flags, h_out, z
+        self.h_out, self.z = h_out, z
         self.keep = (y, h, w_post, w_pre, gate)
         p = [None if t is None else t.data_ptr() for t in (y, h, gate, w_post, w_pre, h_out, z)]
         # an expanded tensor's row stride may be 0 or overlap: the library refuses it
@@ -720,12 +736,8 @@ class NormGateResidual(_Plan):
             raise ValueError("a gate for every row must have rows of its own; pass [n] for one gate")
         self.args = NormArgs(*p, *s, rows, n, _DTYPES[dtype], _DTYPES[h.dtype], float(eps), float(w_offset),
                              float(res_scale))
-        self.refs = (ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p),)
-        self.fn = lib().rmsnorm_gate_residual
-
-    def run(self):
-        self._enqueue(self.fn, "rmsnorm_gate_residual", *self.refs)
-        return self.h_out, self.z
+        self._bind(dev, lib().rmsnorm_gate_residual, "rmsnorm_gate_residual",
+                   (ctypes.cast(ctypes.pointer(self.args), ctypes.c_void_p), flags), (h_out, z))
 
 
 def rmsnorm_gate_residual(y, h, w_post=None, w_pre=None, gate=None, res_scale: float = 1.0, eps: float = 1e-6,

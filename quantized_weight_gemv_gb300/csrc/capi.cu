@@ -186,6 +186,9 @@ int check_grouped(int bits, const qg_gemv_desc* descs, int count, int* active) {
     return QG_OK;
 }
 
+// The cache, attention and norm kernels read and write nothing before griddepcontrol.wait,
+// so their calls are always launched as programmatic dependents: only the launch itself
+// overlaps the preceding work's end (QG_FLAG_PDL adds nothing to them).
 static bool pow2_in(int v, int lo, int hi) { return v >= lo && v <= hi && (v & (v - 1)) == 0; }
 
 static int check_kv8_cache(const qg_kv8_cache* c) {
@@ -500,9 +503,20 @@ int kv8_rope_append(const qg_kv8_cache* cache, const qg_kv8_append_args* a, unsi
     if (rc == QG_OK && a->q) rc = check_kv8_rows(a->q_out, a->q_out_stride, a->n_q_heads, cache->head_dim, a->dtype);
     if (rc != QG_OK) return rc;
     LaunchCtx lc;
-    rc = resolve(stream, flags, lc);
+    rc = resolve(stream, flags | QG_FLAG_PDL, lc);
     if (rc != QG_OK) return rc;
     return launch_kv8_append(*cache, *a, lc);
+}
+
+int kv8_values(const qg_kv8_cache* cache, float* k_out, float* v_out, unsigned flags, void* stream) {
+    int rc = check_kv8_cache(cache);
+    if (rc != QG_OK) return rc;
+    if (!k_out && !v_out) return QG_ERR_INVALID_ARG;
+    if (!aligned16(k_out) || !aligned16(v_out)) return QG_ERR_ALIGNMENT;
+    LaunchCtx lc;
+    rc = resolve(stream, flags | QG_FLAG_PDL, lc);
+    if (rc != QG_OK) return rc;
+    return launch_kv8_values(*cache, k_out, v_out, lc);
 }
 
 size_t kv8_attention_workspace_bytes(int head_dim) {
@@ -525,7 +539,7 @@ int kv8_attention(const qg_kv8_cache* cache, const qg_kv8_attention_args* a, voi
     if (!ws || ws_bytes < kv8_ws_bytes(cache->head_dim)) return QG_ERR_WORKSPACE;
     if (!aligned16(ws)) return QG_ERR_ALIGNMENT;
     LaunchCtx lc;
-    rc = resolve(stream, flags, lc);
+    rc = resolve(stream, flags | QG_FLAG_PDL, lc);
     if (rc != QG_OK) return rc;
     return launch_kv8_attention(*cache, *a, reinterpret_cast<unsigned char*>(ws), lc);
 }
@@ -547,7 +561,7 @@ int rmsnorm_gate_residual(const qg_norm_args* a, unsigned flags, void* stream) {
         off(a->h_out, r))
         return QG_ERR_ALIGNMENT;
     LaunchCtx lc;
-    int rc = resolve(stream, flags, lc);
+    int rc = resolve(stream, flags | QG_FLAG_PDL, lc);
     if (rc != QG_OK) return rc;
     return launch_norm(*a, lc);
 }

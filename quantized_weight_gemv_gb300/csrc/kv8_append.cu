@@ -6,7 +6,7 @@
 // magnitude, and writes the codes against the block's scale - one read of the inputs and
 // one write of the codes, nothing kept between.  A block that already holds tokens is
 // rewritten only when its scale grows, and only that block's bytes (scale_block x
-// head_dim).  The remaining CTAs rotate queries, eight values a thread.
+// head_dim).  The remaining CTAs rotate queries, eight values of four heads a thread.
 #include "kv8.cuh"
 
 namespace qg {
@@ -223,20 +223,27 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
     if (tid == 0) *scale_at = s_new;  // after the barrier above: every thread has read the old one
 }
 
+constexpr int Q_HEADS = 4;  // query heads per thread: they share the row of the tables
+
 template <int D, typename T, bool HALF>
-__device__ __forceinline__ void q_unit(const AppendParams& p, long long item) {
+__device__ __forceinline__ void q_unit(const AppendParams& p, unsigned item) {
     constexpr int SPT = D / 8;
     const int sl = (int)(item % SPT);
-    const long long th = item / SPT;
-    const int t = (int)(th / p.hq), h = (int)(th % p.hq);
+    const unsigned groups = (unsigned)(p.hq + Q_HEADS - 1) / Q_HEADS, th = item / SPT;
+    const int t = (int)(th / groups), h0 = (int)(th % groups) * Q_HEADS;
     if (t >= p.tokens) return;
     int at, bt;
     slot_places<HALF>(sl, p.rot, at, bt);
-    const T* row = reinterpret_cast<const T*>(p.q) + t * p.q_stride + h * D;
-    T* out = reinterpret_cast<T*>(p.q_out) + t * p.q_out_stride + h * D;
-    float x[8];
-    load4(row + at, x);
-    load4(row + bt, x + 4);
+    const T* row = reinterpret_cast<const T*>(p.q) + t * p.q_stride + h0 * D;
+    T* out = reinterpret_cast<T*>(p.q_out) + t * p.q_out_stride + h0 * D;
+    const int heads = min(Q_HEADS, p.hq - h0);
+    float x[Q_HEADS][8];
+#pragma unroll
+    for (int i = 0; i < Q_HEADS; ++i)
+        if (i < heads) {
+            load4(row + i * D + at, x[i]);
+            load4(row + i * D + bt, x[i] + 4);
+        }
     if (8 * sl < p.rot) {
         int r = -1;
         if (p.positions) {
@@ -257,11 +264,19 @@ __device__ __forceinline__ void q_unit(const AppendParams& p, long long item) {
             }
             r = table_row(p, t, p.kv_len[b] - end + t);
         }
-        if (r >= 0)
-            rotate_slot<HALF>(x, p.cos + (long long)r * (p.rot >> 1), p.sin + (long long)r * (p.rot >> 1), sl);
+        if (r >= 0) {
+            const float* cs = p.cos + (long long)r * (p.rot >> 1);
+            const float* sn = p.sin + (long long)r * (p.rot >> 1);
+#pragma unroll
+            for (int i = 0; i < Q_HEADS; ++i) rotate_slot<HALF>(x[i], cs, sn, sl);
+        }
     }
-    store4(out + at, x);
-    store4(out + bt, x + 4);
+#pragma unroll
+    for (int i = 0; i < Q_HEADS; ++i)
+        if (i < heads) {
+            store4(out + i * D + at, x[i]);
+            store4(out + i * D + bt, x[i] + 4);
+        }
 }
 
 template <int D, int FMT, typename T, bool HALF>
@@ -273,7 +288,7 @@ __global__ void append_kernel(const AppendParams p) {
     if ((int)blockIdx.x < units)
         kv_unit<D, FMT, T, HALF>(p, blockIdx.x, red);
     else
-        q_unit<D, T, HALF>(p, (long long)(blockIdx.x - units) * blockDim.x + threadIdx.x);
+        q_unit<D, T, HALF>(p, (blockIdx.x - units) * blockDim.x + threadIdx.x);
 }
 
 template <int D, int FMT, typename T>
@@ -281,9 +296,9 @@ static int launch_d(const AppendParams& p, bool half, const LaunchCtx& lc) {
     // one thread per SLOTS slots of a whole block, two warps at least
     const int nt = max(64, (D / 8 << p.c.block_log2) / SLOTS);
     const long long units = (long long)p.kv_ctas * 2 * p.c.hkv;
-    const long long items = p.q ? (long long)p.tokens * p.hq * (D / 8) : 0;
+    const long long items = p.q ? (long long)p.tokens * ((p.hq + Q_HEADS - 1) / Q_HEADS) * (D / 8) : 0;
     const long long grid = units + (items + nt - 1) / nt;
-    if (grid > 0x7fffffffll) return QG_ERR_UNSUPPORTED;
+    if (grid > 0x7fffffffll || items > 0x7fffffffll) return QG_ERR_UNSUPPORTED;
     return half ? launch_kernel(append_kernel<D, FMT, T, true>, dim3((unsigned)grid), dim3(nt), 0, lc, p)
                 : launch_kernel(append_kernel<D, FMT, T, false>, dim3((unsigned)grid), dim3(nt), 0, lc, p);
 }
@@ -300,7 +315,42 @@ static int launch_t(const AppendParams& p, int d, bool half, const LaunchCtx& lc
     }
 }
 
+// The values that the codes stand for: 16 codes a thread, grid.y 0 for keys and 1 for values.
+template <int FMT>
+__global__ void values_kernel(const CacheView c, float* k_out, float* v_out, long long vecs, int d_log2) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+    float* out = blockIdx.y ? v_out : k_out;
+    if (i >= vecs || !out) return;
+    const uint4 w = reinterpret_cast<const uint4*>(blockIdx.y ? c.v : c.k)[i];
+    const float s = (blockIdx.y ? c.vs : c.ks)[(i << 4 >> d_log2) >> c.block_log2];
+    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t b = (ws[j] >> (8 * e)) & 255u;
+            x[e] = s * (FMT == QG_KV8_INT8 ? (float)(int8_t)b
+                                           : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3))));
+        }
+        store4(out + i * 16 + 4 * j, x);
+    }
+}
+
 }  // namespace kv8
+
+int launch_kv8_values(const qg_kv8_cache& c, float* k_out, float* v_out, const LaunchCtx& lc) {
+    using namespace kv8;
+    const long long vecs = (long long)c.n_pages * c.n_kv_heads * c.page_size * c.head_dim / 16;
+    const long long grid = (vecs + 255) / 256;
+    if (grid > 0x7fffffffll) return QG_ERR_UNSUPPORTED;
+    const dim3 g((unsigned)grid, 2);
+    return c.format == QG_KV8_INT8
+               ? launch_kernel(values_kernel<QG_KV8_INT8>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, vecs, ilog2(c.head_dim))
+               : launch_kernel(values_kernel<QG_KV8_E4M3>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, vecs, ilog2(c.head_dim));
+}
 
 int launch_kv8_append(const qg_kv8_cache& c, const qg_kv8_append_args& a, const LaunchCtx& lc) {
     using namespace kv8;

@@ -87,9 +87,24 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& p01, uint32_
     }
 }
 
+// 2, 4 or 8 consecutive values
+template <typename T, int N>
+__device__ __forceinline__ void load_values(const T* p, float (&x)[N]) {
+    if constexpr (N == 8) {
+        load8(p, x);
+    } else if constexpr (N == 4) {
+        load4(p, x);
+    } else if constexpr (sizeof(T) == 4) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+        unpack2(p, *reinterpret_cast<const uint32_t*>(p), x[0], x[1]);
+    }
+}
+
 // ---------------------------------------------------------------- the shared work list
-// Sequence b has hkv * qt_b row tiles of nt_b token tiles each; ends[b] counts the units of
-// sequences 0..b.
+// Sequence b has hkv * qt_b row tiles of nt_b token tiles each, cut into units of one or a few
+// token tiles; ends[b] counts the units of sequences 0..b.
 struct SeqInfo {
     int t0, n, len;  // first token of the call, tokens of the call, tokens in the cache
     int qt, nt;      // row tiles per kv head, token tiles per row tile
@@ -116,12 +131,13 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     return s;
 }
 
-// what a CTA's merge needs in shared memory beside the row tile's own arrays
 template <int D, int NT>
 struct Shape {
     static constexpr int RT = 8 * NT;                 // query rows per tile
     static constexpr int QUADS = D * NT / 16;         // groups of four values (per lane) of a row tile's output
-    static constexpr size_t merge_bytes = (size_t)W * RT * D * 4;
+    // the warps' shares of a row tile, or the (reference, sum) pairs of its partials
+    static constexpr size_t merge_bytes = (size_t)W * RT * D * 4 > (size_t)MAX_CTAS * RT * 8 ? (size_t)W * RT * D * 4
+                                                                                             : (size_t)MAX_CTAS * RT * 8;
 };
 
 // One quad of the output: lane (g, t) holds d..d+3 of one column of the row tile.
@@ -148,10 +164,9 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint2 qf[PIECES][NT][MT][32];         // query fragments, in the order the MMAs read them
     __shared__ float row_factor[RT];                 // 2^e * scale (* log2 e, or / softcap)
-    __shared__ int row_hi[RT], row_lo[RT];           // visible positions row_lo .. row_hi
     __shared__ float wm[W][RT], wl[W][RT], wv[W];    // per warp: reference, sum, value-scale reference
     __shared__ float tile_m[RT], tile_l[RT];
-    __shared__ long long total_s;
+    __shared__ long long wsum[W];
     __shared__ int last_s;
     long long* ends = reinterpret_cast<long long*>(smem);  // before the first row tile, then kept past the merge area
     float* merge = reinterpret_cast<float*>(smem + (((size_t)p.c.batch * 8 + 15) & ~(size_t)15));
@@ -160,35 +175,45 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
     pdl_wait();
     pdl_launch_dependents();
 
-    // prefix sums of the sequences' units
-    {
-        __shared__ long long wsum[W];
-        long long carry = 0;
-        for (int s = 0; s < p.c.batch; s += W * 32) {
-            long long u = 0;
-            if (s + tid < p.c.batch) {
-                const SeqInfo si = seq_info<RT>(p, s + tid);
-                u = (long long)p.c.hkv * si.qt * si.nt;
-            }
+    // Prefix sums of the sequences' units.  A unit is one token tile while the list is long;
+    // a list of at most four tiles per CTA is cut into units of 1, 2 or 4 tiles, the first
+    // that gives every CTA at most one unit: no CTA then starts a second row tile, whose
+    // fixed costs are several tiles' worth.
+    long long total = 0;
+    int unit = 1;
+    const SeqInfo only = seq_info<RT>(p, 0);  // a lone sequence is looked up once
+    auto units_of = [&](int b) {
+        const SeqInfo si = p.c.batch == 1 ? only : seq_info<RT>(p, b);
+        return (long long)p.c.hkv * si.qt * ((si.nt + unit - 1) / unit);
+    };
+    while (true) {
+        total = 0;
+        if (p.c.batch == 1) {
+            total = units_of(0);
+        } else {
+            for (int s = 0; s < p.c.batch; s += W * 32) {
+                long long u = s + tid < p.c.batch ? units_of(s + tid) : 0;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long v = __shfl_up_sync(0xffffffffu, u, o);
-                if (lane >= o) u += v;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long v = __shfl_up_sync(0xffffffffu, u, o);
+                    if (lane >= o) u += v;
+                }
+                if (lane == 31) wsum[w] = u;
+                __syncthreads();
+                long long base = total;
+                for (int i = 0; i < W; ++i) {
+                    if (i < w) base += wsum[i];
+                    total += wsum[i];
+                }
+                if (s + tid < p.c.batch) ends[s + tid] = base + u;
+                __syncthreads();
             }
-            if (lane == 31) wsum[w] = u;
-            __syncthreads();
-            long long base = carry;
-            for (int i = 0; i < W; ++i) {
-                if (i < w) base += wsum[i];
-                carry += wsum[i];
-            }
-            if (s + tid < p.c.batch) ends[s + tid] = base + u;
-            __syncthreads();
         }
-        if (tid == 0) total_s = carry;
-        __syncthreads();
+        if (total <= gridDim.x) break;
+        if (unit == 1 && total > 4ll * gridDim.x) break;
+        if (unit == 4) break;  // one more cut would idle half the CTAs: as it is
+        unit *= 2;
     }
-    const long long total = total_s;
     const long long ctas = min((long long)gridDim.x, total);
     if (blockIdx.x >= ctas) return;
     long long pos = total * blockIdx.x / ctas;
@@ -196,7 +221,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
     const long long my_start = pos;
 
     while (pos < end) {
-        // the sequence of this unit, its row tile and the run of token tiles taken here
+        // the sequence of this unit, its row tile and the run of units taken here
         int b = 0;
         {
             int hi = p.c.batch - 1;
@@ -208,101 +233,26 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                     b = mid + 1;
             }
         }
-        const SeqInfo si = seq_info<RT>(p, b);
+        const SeqInfo si = p.c.batch == 1 ? only : seq_info<RT>(p, b);
         const long long base = b ? ends[b - 1] : 0;
-        const int seg = (int)((pos - base) / si.nt), tile0 = (int)((pos - base) % si.nt);
-        const int count = (int)min((long long)(si.nt - tile0), end - pos);
-        const long long seg_start = pos - tile0;
+        const int nu = (si.nt + unit - 1) / unit;  // units of a row tile
+        const int seg = (int)((pos - base) / nu), unit0 = (int)((pos - base) % nu);
+        const int count = (int)min((long long)(nu - unit0), end - pos);
+        const long long seg_start = pos - unit0;
         const int h = seg / si.qt, qt = seg % si.qt;
 
-        // ---- the tile's queries
         const int rows = min(RT, si.n * p.group - qt * RT);
-        __syncthreads();  // the previous row tile's shared arrays are no longer read
-        for (int col = w; col < RT; col += W) {
-            const int r = qt * RT + col;
-            const bool valid = col < rows;
-            const int i = valid ? r / p.group : 0, hh = h * p.group + (valid ? r % p.group : 0);
-            constexpr int PER = D / 32;  // values per lane, consecutive
-            float x[PER];
-#pragma unroll
-            for (int e = 0; e < PER; ++e) x[e] = 0.0f;
-            if (valid) {
-                const long long at = (si.t0 + i) * p.q_stride + (long long)hh * D + lane * PER;
-#pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    if constexpr (PIECES == 2)
-                        x[e] = reinterpret_cast<const float*>(p.q)[at + e];
-                    else
-                        x[e] = p.dtype == QG_DTYPE_F16 ? __half2float(reinterpret_cast<const __half*>(p.q)[at + e])
-                                                       : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.q)[at + e]);
-                }
-            }
-            float a = 0.0f;
-#pragma unroll
-            for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[e]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
-            const float down = ldexpf(1.0f, -ex);
-#pragma unroll
-            for (int e = 0; e < PER; e += 2) {
-                // value d: k-step (d / 64) * 4 + d % 16 / 4, lane 4 (col % 8) + d % 64 / 16, register d % 4 / 2
-                const int d = lane * PER + e;
-                const int ks = (d >> 6) * 4 + ((d & 15) >> 2), ln = (col & 7) * 4 + ((d & 63) >> 4), rg = (d & 3) >> 1;
-                const float u = x[e] * down, v = x[e + 1] * down;
-                const __half2 hi2 = __floats2half2_rn(u, v);
-                reinterpret_cast<uint32_t*>(&qf[0][col >> 3][ks][ln])[rg] = *reinterpret_cast<const uint32_t*>(&hi2);
-                if constexpr (PIECES == 2)
-                    reinterpret_cast<uint32_t*>(&qf[PIECES - 1][col >> 3][ks][ln])[rg] =
-                        half2_bits(u - __low2float(hi2), v - __high2float(hi2));
-            }
-            if (lane == 0) {
-                const int at = si.len - si.n + i;
-                const bool ok = valid && at >= 0 && at < si.len;
-                row_hi[col] = ok ? at : -1;
-                row_lo[col] = p.window > 0 ? max(0, at - p.window + 1) : 0;
-                row_factor[col] = ldexpf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f, ex);
-            }
-        }
-        __syncthreads();
-
-        // ---- this warp's state
-        float o[MT][NT][4];
-        float mo[NT][2], l[NT][2], rf[NT][2];
-        int hi_c[NT][2], lo_c[NT][2];
-        int hi_min = 0x7fffffff, hi_max = -1, lo_min = 0x7fffffff, lo_max = 0;
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int col = 8 * n + 2 * t + i;
-                mo[n][i] = -1e30f;
-                l[n][i] = 0.0f;
-                rf[n][i] = row_factor[col];
-                hi_c[n][i] = row_hi[col];
-                lo_c[n][i] = row_lo[col];
-            }
-        for (int r = 0; r < rows; ++r) {
-            const int hi = row_hi[r], lo = row_lo[r];
-            hi_min = min(hi_min, hi);
-            if (hi < 0) continue;
-            hi_max = max(hi_max, hi);
-            lo_min = min(lo_min, lo);
-            lo_max = max(lo_max, lo);
-        }
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) o[m][n][i] = 0.0f;
-        float vref = 0.0f, vref_inv = 0.0f;  // power of two that the value scales are relative to
-        const float cap2 = p.softcap * 1.44269504088896f;
+        // positions of the tile's first and last token (negative: sees nothing), and what some
+        // row sees (lo_min .. hi_max) and every row sees (lo_max .. hi_min)
+        const int at0 = si.len - si.n + qt * RT / p.group, at1 = si.len - si.n + (qt * RT + rows - 1) / p.group;
+        const int hi_min = at0, hi_max = at1;
+        const int lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
+        const int lo_max = p.window > 0 ? max(0, at1 - p.window + 1) : 0;
 
         // ---- cache tokens, 16 per step: steps first + w, + W, ... of this run's tiles
         const int origin = hi_max < 0 ? 0 : lo_min & ~(SUB - 1);
-        const int last_tok = min(hi_max + 1, origin + (tile0 + count) * W * SUB);  // one past
-        int tok = origin + (tile0 * W + w) * SUB;
+        const int last_tok = min(hi_max + 1, origin + (unit0 + count) * unit * W * SUB);  // one past
+        int tok = origin + (unit0 * unit * W + w) * SUB;
         const int32_t* table = p.c.table + (long long)b * p.c.max_pages;
         const int pmask = (1 << p.c.page_log2) - 1;
 
@@ -346,15 +296,86 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             load_k(s);
             load_v(s);
         }
+        // ---- the tile's queries
+        __syncthreads();  // the previous row tile's shared arrays are no longer read
+        for (int col = w; col < RT; col += W) {
+            const int r = qt * RT + col;
+            const bool valid = col < rows;
+            const int i = valid ? r / p.group : 0, hh = h * p.group + (valid ? r % p.group : 0);
+            constexpr int PER = D / 32;  // values per lane, consecutive
+            float x[PER];
+#pragma unroll
+            for (int e = 0; e < PER; ++e) x[e] = 0.0f;
+            if (valid) {
+                const long long at = (si.t0 + i) * p.q_stride + (long long)hh * D + lane * PER;
+                if constexpr (PIECES == 2)
+                    load_values(reinterpret_cast<const float*>(p.q) + at, x);
+                else if (p.dtype == QG_DTYPE_F16)
+                    load_values(reinterpret_cast<const __half*>(p.q) + at, x);
+                else
+                    load_values(reinterpret_cast<const __nv_bfloat16*>(p.q) + at, x);
+            }
+            float a = 0.0f;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[e]));
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
+            const float down = ldexpf(1.0f, -ex);
+#pragma unroll
+            for (int e = 0; e < PER; e += 2) {
+                // value d: k-step (d / 64) * 4 + d % 16 / 4, lane 4 (col % 8) + d % 64 / 16, register d % 4 / 2
+                const int d = lane * PER + e;
+                const int ks = (d >> 6) * 4 + ((d & 15) >> 2), ln = (col & 7) * 4 + ((d & 63) >> 4), rg = (d & 3) >> 1;
+                const float u = x[e] * down, v = x[e + 1] * down;
+                const __half2 hi2 = __floats2half2_rn(u, v);
+                reinterpret_cast<uint32_t*>(&qf[0][col >> 3][ks][ln])[rg] = *reinterpret_cast<const uint32_t*>(&hi2);
+                if constexpr (PIECES == 2)
+                    reinterpret_cast<uint32_t*>(&qf[PIECES - 1][col >> 3][ks][ln])[rg] =
+                        half2_bits(u - __low2float(hi2), v - __high2float(hi2));
+            }
+            if (lane == 0)
+                row_factor[col] = ldexpf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f, ex);
+        }
+        __syncthreads();
+
+        // ---- this warp's state
+        float o[MT][NT][4];
+        float mo[NT][2], l[NT][2], rf[NT][2];
+        int hi_c[NT][2], lo_c[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int col = 8 * n + 2 * t + i;
+                mo[n][i] = -1e30f;
+                l[n][i] = 0.0f;
+                rf[n][i] = row_factor[col];
+                const int at = si.len - si.n + (qt * RT + col) / p.group;
+                hi_c[n][i] = at;
+                lo_c[n][i] = p.window > 0 ? at - p.window + 1 : 0;
+            }
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[m][n][i] = 0.0f;
+        float vref = 0.0f, vref_inv = 0.0f;  // power of two that the value scales are relative to
+        const float cap2 = p.softcap * 1.44269504088896f;
+
         while (tok < last_tok) {
             const int next = tok + W * SUB;
             const long long slot_next = slot_of(page_next, next);
             bool bad = (unsigned)page >= (unsigned)p.c.n_pages;
             if (bad && lane == 0) atomicOr(p.err, ERR_KV_RANGE);
             // scores
-            float s[NT][4];
+            // (two sums per row tile: the matrix instructions of one are a chain)
+            float s[NT][4], s2[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) s[n][i] = s2[n][i] = 0.0f;
 #pragma unroll
             for (int c = 0; c < KC; ++c) {
                 const uint32_t* k0 = reinterpret_cast<const uint32_t*>(&kr[0][c]);
@@ -369,7 +390,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
 #pragma unroll
                         for (int pc = 0; pc < PIECES; ++pc) {
                             const uint2 f = qf[pc][n][c * 4 + u][lane];
-                            mma16816(s[n], a, f.x, f.y);
+                            mma16816(PIECES == 2 ? (pc ? s2[n] : s[n]) : (u & 1 ? s2[n] : s[n]), a, f.x, f.y);
                         }
                 }
             }
@@ -382,7 +403,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float x = s[n][i] * (rf[n][i & 1] * ks_now);
+                    float x = (s[n][i] + s2[n][i]) * (rf[n][i & 1] * ks_now);
                     if (p.softcap > 0.0f) x = cap2 * tanhf(x);
                     s[n][i] = x;
                 }
@@ -514,14 +535,13 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
         }
         __syncthreads();
 
-        const bool whole = count == si.nt;
+        const bool whole = count == nu;
         // a run that continues the previous CTA's row tile goes to its first slot, one that
         // the next CTA continues to its second
         const int slot_id = 2 * blockIdx.x + (seg_start >= my_start ? 1 : 0);
         auto write_row = [&](int quad, float4 v) {
             int n, col, d;
             quad_place<D>(quad, lane, n, col, d);
-            if (col >= rows) return;
             const float sum = tile_l[col];
             const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
             const int r = qt * RT + col;
@@ -545,6 +565,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
         for (int quad = w; quad < S::QUADS; quad += W) {
             int n, col, d;
             quad_place<D>(quad, lane, n, col, d);
+            if (col >= rows) continue;
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int i = 0; i < W; ++i) {
@@ -566,7 +587,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             }
             // the CTAs of this row tile: those that hold its first and its last unit
             const int c0 = (int)(((seg_start + 1) * ctas - 1) / total);
-            const int c1 = (int)(((seg_start + si.nt) * ctas - 1) / total);
+            const int c1 = (int)(((seg_start + nu) * ctas - 1) / total);
             __threadfence();
             __syncthreads();
             if (tid == 0) {
@@ -581,27 +602,39 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                 auto slot_of_cta = [&](int c) {
                     return (size_t)(2 * c + (c == c0 ? 1 : 0));  // only c0 begins the row tile
                 };
-                if (tid < RT) {
-                    float m = -1e30f;
-                    for (int c = c0; c <= c1; ++c) m = fmaxf(m, __ldcg(p.part_ml + (slot_of_cta(c) * RT + tid) * 2));
-                    float sum = 0.0f;
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* at = p.part_ml + (slot_of_cta(c) * RT + tid) * 2;
-                        sum += __ldcg(at + 1) * ex2(__ldcg(at) - m);
+                // (reference, sum) of every partial side by side, then a warp per row
+                const int parts = c1 - c0 + 1;
+                float2* ml = reinterpret_cast<float2*>(merge);
+                for (int i = tid; i < parts * RT; i += W * 32)
+                    ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of_cta(c0 + i / RT) * RT + i % RT);
+                __syncthreads();
+                for (int col = w; col < RT; col += W) {
+                    float m = -1e30f, sum = 0.0f;
+                    for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[i * RT + col].x);
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+                    for (int i = lane; i < parts; i += 32) {
+                        const float f = ex2(ml[i * RT + col].x - m);
+                        sum += ml[i * RT + col].y * f;
+                        ml[i * RT + col].x = f;  // now the partial's factor
                     }
-                    tile_m[tid] = m;
-                    tile_l[tid] = sum;
+                    sum = warp_sum(sum);
+                    if (lane == 0) {
+                        tile_m[col] = m;
+                        tile_l[col] = sum;
+                    }
                 }
                 __syncthreads();
                 for (int quad = w; quad < S::QUADS; quad += W) {
                     int n, col, d;
                     quad_place<D>(quad, lane, n, col, d);
-                    const float m = tile_m[col];
+                    if (col >= rows) continue;
                     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    for (int c = c0; c <= c1; ++c) {
-                        const size_t sl = slot_of_cta(c);
-                        const float f = ex2(__ldcg(p.part_ml + (sl * RT + col) * 2) - m);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o) + (sl * S::QUADS + quad) * 32 + lane);
+                    const float4* at = reinterpret_cast<const float4*>(p.part_o) + (size_t)quad * 32 + lane;
+#pragma unroll 8
+                    for (int i = 0; i < parts; ++i) {
+                        const float4 v = __ldcg(at + slot_of_cta(c0 + i) * S::QUADS * 32);
+                        const float f = ml[i * RT + col].x;
                         acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
                     }
                     write_row(quad, acc);

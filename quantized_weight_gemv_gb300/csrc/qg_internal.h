@@ -147,6 +147,7 @@ int launch_chain(int bits, const qg_gemv_desc* descs, int count, const int* phas
 int launch_select(const float* logits, int n, const int32_t* allowed, int n_allowed, int32_t* token, float* logprob,
                   SelectWorkspace* ws, const LaunchCtx& lc);
 int launch_kv8_append(const qg_kv8_cache& c, const qg_kv8_append_args& a, const LaunchCtx& lc);
+int launch_kv8_values(const qg_kv8_cache& c, float* k_out, float* v_out, const LaunchCtx& lc);
 size_t kv8_ws_bytes(int head_dim);
 int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, unsigned char* ws, const LaunchCtx& lc);
 int launch_norm(const qg_norm_args& a, const LaunchCtx& lc);
