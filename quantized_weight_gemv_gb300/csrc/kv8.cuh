@@ -103,5 +103,96 @@ __device__ __forceinline__ void from_float(float v, float& x) { x = v; }
 __device__ __forceinline__ void from_float(float v, __half& x) { x = __float2half_rn(v); }
 __device__ __forceinline__ void from_float(float v, __nv_bfloat16& x) { x = __float2bfloat16_rn(v); }
 
+// 2, 4 or 8 consecutive values
+template <typename T, int N>
+__device__ __forceinline__ void load_values(const T* p, float (&x)[N]) {
+    if constexpr (N == 8) {
+        load8(p, x);
+    } else if constexpr (N == 4) {
+        load4(p, x);
+    } else if constexpr (sizeof(T) == 4) {
+        const float2 v = *reinterpret_cast<const float2*>(p);
+        x[0] = v.x, x[1] = v.y;
+    } else {
+        unpack2(p, *reinterpret_cast<const uint32_t*>(p), x[0], x[1]);
+    }
+}
+
+// ---------------------------------------------------------------- attention: what both kernels share
+// Weights are held as 2^(x - m + P_BITS): binary16 keeps 11 bits of a weight down to 2^-24 of the largest.
+constexpr float P_BITS = 10.0f;
+constexpr float P_SLACK = 4.0f;  // x may exceed m by this much before m moves
+
+struct AttnParams {
+    CacheView c;
+    const void* q;
+    void* out;
+    float* lse;
+    const int32_t* kv_len;
+    const int32_t* cu;
+    long long q_stride, out_stride;
+    int tokens, hq, group, dtype, window;
+    float scale, softcap;
+    // the split kernel's workspace: arrival counters (zero between calls), and per CTA two
+    // partials: (reference, sum) of each row, and the rows' weighted values
+    unsigned* counter;
+    float* part_ml;
+    float* part_o;
+    unsigned* err;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
+    const __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes (bytes of w) as binary16 pairs (b0, b1) and (b2, b3).  int8: code + 128 as the
+// low byte of the binary16 1024 + (code + 128), less 1152: exact.  e4m3: a conversion.
+template <int FMT>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& p01, uint32_t& p23) {
+    if constexpr (FMT == QG_KV8_INT8) {
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
+        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+        p01 = *reinterpret_cast<const uint32_t*>(&x);
+        p23 = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        asm("{.reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;}"
+            : "=r"(p01), "=r"(p23)
+            : "r"(w));
+    }
+}
+
+// Sequence b of a call: its first token, its tokens, the tokens it holds in the cache.  A
+// range that does not fit the call or the page table is reported and counts as empty.
+struct Sequence {
+    int t0, n, len;
+};
+__device__ __forceinline__ Sequence sequence(const AttnParams& p, int b) {
+    Sequence s;
+    s.t0 = p.cu ? p.cu[b] : b;
+    s.n = p.cu ? p.cu[b + 1] - s.t0 : 1;
+    s.len = p.kv_len[b];
+    if (s.t0 < 0 || s.n < 0 || s.t0 + (long long)s.n > p.tokens) {
+        atomicOr(p.err, ERR_KV_RANGE);
+        s.n = 0;
+    }
+    if (s.len > ((long long)p.c.max_pages << p.c.page_log2) || s.len < 0) {
+        atomicOr(p.err, ERR_KV_RANGE);
+        s.len = 0;
+    }
+    return s;
+}
+
+// many query rows per kv head (kv8_prefill.cu)
+int launch_prefill(const AttnParams& p, int format, int d, const LaunchCtx& lc);
+
 }  // namespace kv8
 }  // namespace qg

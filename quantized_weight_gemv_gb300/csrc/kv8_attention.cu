@@ -24,33 +24,10 @@ namespace kv8 {
 
 constexpr int W = 8;            // warps per CTA
 constexpr int SUB = 16;         // cache tokens per warp step
+constexpr int PREFILL_ROWS = 64;  // query rows per sequence and kv head from which launch_prefill takes the call
 constexpr int MAX_CTAS = 320;   // CTAs that share out one call (workspace slots)
-constexpr float P_BITS = 10.0f; // p is held as 2^(x - m + P_BITS)
-constexpr float P_SLACK = 4.0f; // x may exceed m by this much before m moves
-
-struct AttnParams {
-    CacheView c;
-    const void* q;
-    void* out;
-    float* lse;
-    const int32_t* kv_len;
-    const int32_t* cu;
-    long long q_stride, out_stride;
-    int tokens, hq, group, dtype, window;
-    float scale, softcap;
-    unsigned* counter;  // [MAX_CTAS], zero between calls
-    float* part_ml;     // [2 * MAX_CTAS][rows][2]
-    float* part_o;      // [2 * MAX_CTAS][rows * D]
-    unsigned* err;
-};
 
 // ---------------------------------------------------------------- device helpers
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -64,66 +41,16 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
     return r;
 }
 
-__device__ __forceinline__ uint32_t half2_bits(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Four codes (bytes of w) as binary16 pairs (b0, b1) and (b2, b3).  int8: code + 128 as the
-// low byte of the binary16 1024 + (code + 128), less 1152: exact.  e4m3: a conversion.
-template <int FMT>
-__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& p01, uint32_t& p23) {
-    if constexpr (FMT == QG_KV8_INT8) {
-        const uint32_t u = w ^ 0x80808080u;
-        const __half2 off = __half2half2(__ushort_as_half((unsigned short)0x6480));  // 1152
-        uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
-        const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
-        p01 = *reinterpret_cast<const uint32_t*>(&x);
-        p23 = *reinterpret_cast<const uint32_t*>(&y);
-    } else {
-        asm("{.reg .b16 lo, hi;\n mov.b32 {lo, hi}, %2;\n cvt.rn.f16x2.e4m3x2 %0, lo;\n cvt.rn.f16x2.e4m3x2 %1, hi;}"
-            : "=r"(p01), "=r"(p23)
-            : "r"(w));
-    }
-}
-
-// 2, 4 or 8 consecutive values
-template <typename T, int N>
-__device__ __forceinline__ void load_values(const T* p, float (&x)[N]) {
-    if constexpr (N == 8) {
-        load8(p, x);
-    } else if constexpr (N == 4) {
-        load4(p, x);
-    } else if constexpr (sizeof(T) == 4) {
-        const float2 v = *reinterpret_cast<const float2*>(p);
-        x[0] = v.x, x[1] = v.y;
-    } else {
-        unpack2(p, *reinterpret_cast<const uint32_t*>(p), x[0], x[1]);
-    }
-}
-
 // ---------------------------------------------------------------- the shared work list
 // Sequence b has hkv * qt_b row tiles of nt_b token tiles each, cut into units of one or a few
 // token tiles; ends[b] counts the units of sequences 0..b.
-struct SeqInfo {
-    int t0, n, len;  // first token of the call, tokens of the call, tokens in the cache
-    int qt, nt;      // row tiles per kv head, token tiles per row tile
+struct SeqInfo : Sequence {
+    int qt, nt;  // row tiles per kv head, token tiles per row tile
 };
 
 template <int RT>
 __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
-    SeqInfo s;
-    s.t0 = p.cu ? p.cu[b] : b;
-    s.n = p.cu ? p.cu[b + 1] - s.t0 : 1;
-    s.len = p.kv_len[b];
-    if (s.t0 < 0 || s.n < 0 || s.t0 + (long long)s.n > p.tokens) {
-        atomicOr(p.err, ERR_KV_RANGE);
-        s.n = 0;
-    }
-    if (s.len > ((long long)p.c.max_pages << p.c.page_log2) || s.len < 0) {
-        atomicOr(p.err, ERR_KV_RANGE);
-        s.len = 0;
-    }
+    SeqInfo s{sequence(p, b), 0, 0};
     s.qt = (int)(((long long)s.n * p.group + RT - 1) / RT);
     // the widest row tile: RT rows span at most (RT - 1) / group + 2 tokens
     const int span = p.window > 0 ? min((long long)s.len, (long long)p.window + (RT - 1) / p.group + 1 + SUB) : s.len;
@@ -131,6 +58,7 @@ __device__ __forceinline__ SeqInfo seq_info(const AttnParams& p, int b) {
     return s;
 }
 
+// the row tile and what its merge needs in shared memory
 template <int D, int NT>
 struct Shape {
     static constexpr int RT = 8 * NT;                 // query rows per tile
@@ -699,6 +627,7 @@ int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, 
     p.tokens = a.tokens, p.hq = a.n_q_heads, p.group = a.n_q_heads / c.n_kv_heads, p.dtype = a.dtype;
     p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
     p.err = lc.err;
+    if ((long long)p.tokens * p.group / c.batch >= PREFILL_ROWS) return launch_prefill(p, c.format, c.head_dim, lc);
     const bool f32 = a.dtype == QG_DTYPE_F32;
     if (c.format == QG_KV8_INT8)
         return f32 ? launch_d<QG_KV8_INT8, 2>(p, c.head_dim, ws, lc) : launch_d<QG_KV8_INT8, 1>(p, c.head_dim, ws, lc);

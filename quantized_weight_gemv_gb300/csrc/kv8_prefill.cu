@@ -1,0 +1,661 @@
+// kv8_attention for many query rows per kv head (prompts): tcgen05 matrix instructions.
+//
+// One CTA per (sequence, kv head, R * 128 query rows), rows being (token, grouped head)
+// pairs, so that grouped heads share each cache token.  Per tile of TN cache tokens
+//   S = Q K^T   (128 x TN per row tile, fp32 in TMEM; Q and K binary16 in shared memory)
+//   P = 2^(S * factor - m) * u, binary16, written back over S in TMEM
+//   O += P V    (128 x D, fp32 in TMEM; P from TMEM, V^T binary16 in shared memory)
+// The cache's codes are exact in binary16, so K and V are widened without rounding and the
+// block scales multiply afterwards: K's onto the score, V's (relative to the largest power of
+// two among the CTA's blocks) onto P.  Queries are brought to [-1, 1] by a power of two per
+// row; fp32 queries and weights enter as two binary16 pieces, two products each.
+//
+// Roles (13 warps): one warpgroup per row tile does the softmax, a thread per row; one
+// warpgroup widens the next tile's codes from registers into the 128-byte-swizzled K-major
+// tiles that the matrix instructions read (V transposed on the way: pairs of tokens are
+// interleaved by byte permutes); one thread issues.  R = 2 row tiles (D <= 128) keep the
+// tensor cores on one tile while the other's softmax runs; at D = 256 TMEM holds one row
+// tile and S is double-buffered instead.
+// The softmax reference m moves only when a score leaves it by more than 2^4; O is then
+// rescaled in TMEM by the row's own thread.  Every wait is bounded.
+#include "kv8.cuh"
+
+namespace qg {
+namespace kv8 {
+
+constexpr int PF_THREADS = 416;
+constexpr int PF_ROWS = 128;  // rows of one matrix instruction
+
+template <int D, int PIECES>
+struct Prefill {
+    static constexpr int R = D == 256 ? 1 : 2;            // row tiles per CTA
+    static constexpr int TN = D == 256 ? 64 : 128;        // cache tokens per tile
+    static constexpr int ST = PIECES == 2 && D >= 128 ? 1 : 2;  // K and V buffers
+    static constexpr int Q_BYTES = PF_ROWS * D * 2;       // one piece of one row tile
+    static constexpr int K_BYTES = TN * D * 2;
+    static constexpr int used = R * PIECES * Q_BYTES + ST * 2 * K_BYTES + 1024;
+    static constexpr int smem = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM: each takes all of TMEM
+    static constexpr int O_COL = 2 * TN;                  // TMEM: two S buffers, then R outputs
+    static_assert(O_COL + R * D <= 512, "TMEM columns");
+    static_assert(smem <= 227 * 1024, "shared memory");
+};
+
+// ---------------------------------------------------------------- mbarriers, tcgen05
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(uint64_t* b, unsigned count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(b)), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint64_t* b) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint64_t* b, unsigned parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_addr(b)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// false once the wait has run out here or anywhere in the CTA
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
+    if (bar_try(b, parity)) return true;
+    const unsigned long long t0 = globaltimer_ns();
+    while (!bar_try(b, parity)) {
+        if (*stop) return false;
+        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
+            *stop = 1;
+            atomicOr(err, ERR_WAIT_FULL);
+            return false;
+        }
+    }
+    return true;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* b) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
+}
+// K-major tile of 128-byte rows, 128-byte swizzle, 1024 bytes per group of eight rows
+__device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
+    return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+// binary16 x binary16 -> fp32, both K-major, M = 128
+__host__ __device__ constexpr uint32_t mma_desc(int n) { return (1u << 4) | ((uint32_t)(n >> 3) << 17) | (8u << 24); }
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(desc), "r"((uint32_t)add)
+        : "memory");
+}
+#define QG_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
+#define QG_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
+// 32 columns of the warp's 32 lanes (a lane's row)
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        : QG_R8(v, 0), QG_R8(v, 8), QG_R8(v, 16), QG_R8(v, 24)
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::QG_W8(v, 0),
+        QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::QG_W8(v, 0),
+        QG_W8(v, 8), "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// what the softmax needs of one token tile, in a ring of four
+template <int TN>
+struct TileInfo {
+    float ks[TN / 16];  // K's scale of each 16 tokens
+    float u[TN / 16];   // V's, relative to the CTA's reference
+    int hidden;         // bit i: these 16 tokens could not be read
+};
+
+template <int D, int FMT, int PIECES>
+__global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams p) {
+    using C = Prefill<D, PIECES>;
+    constexpr int R = C::R, TN = C::TN, ST = C::ST, RR = R * PF_ROWS;
+    extern __shared__ unsigned char smem_raw[];
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], pv_done, drained;
+    __shared__ TileInfo<TN> info[4];
+    __shared__ float row_factor[RR];
+    __shared__ unsigned v_top;  // the largest value scale, as bits
+    __shared__ int stop;
+    __shared__ uint32_t tmem_s;
+    unsigned char* base = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char* qs = base;  // [row tile][piece][D / 64][128 rows x 128 B]
+    unsigned char* kst = qs + R * PIECES * C::Q_BYTES;
+    unsigned char* vst = kst + ST * C::K_BYTES;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // the sequence and row tile: sequence b owns the virtual tiles from floor(first row / RR) + b
+    // on; the last ones come first, a causal mask makes them the longest
+    const int vt = (int)(gridDim.x - 1 - blockIdx.x), h = blockIdx.y;
+    auto tile_of = [&](int b) { return (int)((long long)(p.cu ? p.cu[b] : b) * p.group / RR) + b; };
+    int b = 0;
+    for (int hi = p.c.batch; hi - b > 1;) {
+        const int mid = (b + hi) >> 1;
+        if (tile_of(mid) <= vt)
+            b = mid;
+        else
+            hi = mid;
+    }
+    const Sequence sq = sequence(p, b);
+    const long long row0 = (long long)(vt - tile_of(b)) * RR;
+    if (row0 < 0 || row0 >= (long long)sq.n * p.group) return;
+    const int rows = (int)min((long long)RR, (long long)sq.n * p.group - row0);
+    const int pos0 = sq.len - sq.n;  // position of the sequence's first token of the call
+    const int at0 = pos0 + (int)(row0 / p.group), at1 = pos0 + (int)((row0 + rows - 1) / p.group);
+    const int lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
+    const int t_begin = lo_min & ~15, t_end = at1 + 1;
+    const int tiles = t_end > t_begin ? (t_end - t_begin + TN - 1) / TN : 0;
+    const int esize = PIECES == 2 ? 4 : 2;
+
+    auto row_at = [&](const void* basep, long long stride, int r) {  // row r of this CTA in q or out
+        const int rr = (int)row0 + r;
+        return (const unsigned char*)basep +
+               ((sq.t0 + rr / p.group) * stride + (long long)(h * p.group + rr % p.group) * D) * esize;
+    };
+    if (tiles == 0) {  // no row sees anything
+        for (int i = tid; i < rows * (D * esize / 16); i += PF_THREADS) {
+            const int r = i / (D * esize / 16), c = i % (D * esize / 16);
+            reinterpret_cast<uint4*>(const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)))[c] = make_uint4(0, 0, 0, 0);
+            if (p.lse && c == 0)
+                p.lse[(long long)(sq.t0 + (row0 + r) / p.group) * p.hq + h * p.group + (row0 + r) % p.group] = -INFINITY;
+        }
+        return;
+    }
+
+    // ---- set-up: barriers, TMEM, the value scales' reference, the queries
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&k_full[i], 128);
+            bar_init(&v_full[i], 128);
+            bar_init(&k_empty[i], 1);
+            bar_init(&v_empty[i], 1);
+            bar_init(&s_full[i], 2);
+            bar_init(&p_ready[i], 128);
+            bar_init(&o_full[i], 1);
+        }
+        bar_init(&pv_done, 1);
+        bar_init(&drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        v_top = 0u;
+        stop = 0;
+    }
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_s)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncthreads();  // v_top is zero
+    const int32_t* table = p.c.table + (long long)b * p.c.max_pages;
+    const int pmask = (1 << p.c.page_log2) - 1;
+    auto slot_of = [&](int tok, bool& ok) {  // token slot of `tok`, page 0 where it cannot be read
+        const int page = tok < t_end ? table[tok >> p.c.page_log2] : -1;
+        ok = (unsigned)page < (unsigned)p.c.n_pages;
+        return slot_base(p.c, ok ? page : 0, h) + (tok & pmask);
+    };
+    {
+        unsigned top = 0u;
+        for (int tok = t_begin + tid * 16; tok < t_end; tok += PF_THREADS * 16) {
+            bool ok;
+            const long long s = slot_of(tok, ok);
+            const float v = p.c.vs[s >> p.c.block_log2];
+            if (ok && v < INFINITY && v > 0.0f) top = max(top, __float_as_uint(v));
+            if (!ok) atomicOr(p.err, ERR_KV_RANGE);
+        }
+        for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0 && top) atomicMax(&v_top, top);
+    }
+    if (warp < 8) {
+        constexpr int PER = D / 32, BATCH = 8;
+        const float sign = p.scale < 0.0f ? -1.0f : 1.0f;  // the row factor stays positive
+        for (int r0 = warp * (RR / 8); r0 < (warp + 1) * (RR / 8); r0 += BATCH) {
+            float x[BATCH][PER];
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) x[i][e] = 0.0f;
+                if (r0 + i < rows) {
+                    const unsigned char* at = row_at(p.q, p.q_stride, r0 + i) + lane * PER * esize;
+                    if constexpr (PIECES == 2)
+                        load_values(reinterpret_cast<const float*>(at), x[i]);
+                    else if (p.dtype == QG_DTYPE_F16)
+                        load_values(reinterpret_cast<const __half*>(at), x[i]);
+                    else
+                        load_values(reinterpret_cast<const __nv_bfloat16*>(at), x[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int r = r0 + i, rt = r / PF_ROWS, rr = r % PF_ROWS;
+                float a = 0.0f;
+#pragma unroll
+                for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[i][e]));
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
+                const float down = ldexpf(sign, -ex);
+#pragma unroll
+                for (int e = 0; e < PER; e += 2) {
+                    const int d = lane * PER + e;
+                    const float u = x[i][e] * down, v = x[i][e + 1] * down;
+                    const __half2 hi2 = __floats2half2_rn(u, v);
+                    unsigned char* at = qs + rt * PIECES * C::Q_BYTES + (d >> 6) * (PF_ROWS * 128) + rr * 128 +
+                                        ((((d & 63) >> 3) ^ (rr & 7)) << 4) + (d & 7) * 2;
+                    *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(&hi2);
+                    if constexpr (PIECES == 2)
+                        *reinterpret_cast<uint32_t*>(at + C::Q_BYTES) = half2_bits(u - __low2float(hi2), v - __high2float(hi2));
+                }
+                if (lane == 0)
+                    row_factor[r] = ldexpf(fabsf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f), ex);
+            }
+        }
+        fence_async_smem();
+    }
+    tc_before();
+    __syncthreads();
+    tc_after();
+    const uint32_t tmem = tmem_s;
+    const float v_ref = __uint_as_float(v_top & 0x7f800000u);  // a power of two (0: every scale is 0 or subnormal)
+    const float v_inv = v_ref > 0.0f ? 1.0f / v_ref : 0.0f;
+    bool live = true;
+
+    if (warp < 4 * R) {
+        // ================================ softmax: a thread per row
+        const int s = warp >> 2, r = s * PF_ROWS + (warp & 3) * 32 + lane;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const float rf = row_factor[r];
+        const int hi = r < rows ? pos0 + (int)((row0 + r) / p.group) : t_end;  // rows past the end: never masked, never stored
+        const int lo = p.window > 0 && r < rows ? hi - p.window + 1 : 0;
+        // over the warp: tokens that every row sees
+        int hi_min = hi, lo_max = lo;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            hi_min = min(hi_min, __shfl_xor_sync(0xffffffffu, hi_min, o));
+            lo_max = max(lo_max, __shfl_xor_sync(0xffffffffu, lo_max, o));
+        }
+        const float cap2 = p.softcap * 1.44269504088896f;
+        const bool cap = p.softcap > 0.0f;
+        float mo = -1e30f, l = 0.0f;
+        for (int j = 0; j < tiles && live; ++j) {
+            const int buf = R == 2 ? s : j & 1, phase = R == 2 ? j & 1 : (j >> 1) & 1;
+            live = __all_sync(0xffffffffu, bar_wait(&s_full[buf], phase, &stop, p.err));
+            if (!live) break;
+            tc_after();
+            const TileInfo<TN>& ti = info[j & 3];
+            const uint32_t st = lanes + buf * TN;
+            const int tok = t_begin + j * TN;
+            const int hidden = ti.hidden;
+            const bool plain = !cap && !hidden && tok + TN - 1 <= hi_min && tok >= lo_max;
+            // the score of column c (its raw product v) in base 2
+            auto score = [&](float v, int c) {
+                float x = v * (rf * ti.ks[c >> 4]);
+                if (cap) x = cap2 * tanhf(x);
+                const int t = tok + c;
+                return t > hi || t < lo || ((hidden >> (c >> 4)) & 1) ? -INFINITY : x;
+            };
+            // the largest score, to see whether the reference holds
+            float m = -INFINITY;
+            uint32_t hold[PIECES == 2 ? TN / 2 : 1];  // two pieces of P cover all of S: its upper half is kept
+#pragma unroll
+            for (int c = 0; c < TN; c += 32) {
+                uint32_t v[32];
+                tmem_load32(st + c, v);
+                if (plain) {
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        float x = __uint_as_float(v[16 * q]);
+#pragma unroll
+                        for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(v[16 * q + e]));
+                        m = fmaxf(m, x * (rf * ti.ks[c / 16 + q]));
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) m = fmaxf(m, score(__uint_as_float(v[e]), c + e));
+                }
+                if constexpr (PIECES == 2)
+                    if (c >= TN / 2) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) hold[c - TN / 2 + e] = v[e];
+                    }
+            }
+            if (__any_sync(0xffffffffu, m > mo + (P_BITS + P_SLACK))) {
+                const float to = fmaxf(mo, m - P_BITS), f = ex2(mo - to);
+                l *= f;
+                mo = to;
+                if (j > 0) {
+                    if (R == 1) {  // the last product may still be running
+                        live = __all_sync(0xffffffffu, bar_wait(&pv_done, (j - 1) & 1, &stop, p.err));
+                        if (!live) break;
+                        tc_after();
+                    }
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t v[32];
+                        tmem_load32(lanes + C::O_COL + s * D + c, v);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+                        tmem_store32(lanes + C::O_COL + s * D + c, v);
+                    }
+                }
+            }
+            // weights
+#pragma unroll
+            for (int c = 0; c < TN; c += 32) {
+                uint32_t v[32];
+                if (PIECES == 1 || c < TN / 2) {
+                    tmem_load32(st + c, v);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = hold[PIECES == 2 ? c - TN / 2 + e : 0];
+                }
+                uint32_t w[16], w2[16];
+                float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float f = rf * ti.ks[c / 16 + q], u = ti.u[c / 16 + q];
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const int i = 16 * q + e;
+                        float a, z;
+                        if (plain) {
+                            a = ex2(fmaf(__uint_as_float(v[i]), f, -mo));
+                            z = ex2(fmaf(__uint_as_float(v[i + 1]), f, -mo));
+                        } else {
+                            a = ex2(score(__uint_as_float(v[i]), c + i) - mo);
+                            z = ex2(score(__uint_as_float(v[i + 1]), c + i + 1) - mo);
+                        }
+                        l4[e & 2] += a;
+                        l4[(e & 2) + 1] += z;
+                        // a hidden token's weight is 0 whatever its block's scale holds
+                        a = !plain && a == 0.0f ? 0.0f : a * u;
+                        z = !plain && z == 0.0f ? 0.0f : z * u;
+                        const __half2 hi2 = __floats2half2_rn(a, z);
+                        w[i / 2] = *reinterpret_cast<const uint32_t*>(&hi2);
+                        if constexpr (PIECES == 2) w2[i / 2] = half2_bits(a - __low2float(hi2), z - __high2float(hi2));
+                    }
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                tmem_store16(st + c / 2, w);
+                if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + c / 2, w2);
+            }
+            tmem_store_wait();
+            tc_before();
+            bar_arrive(&p_ready[buf]);
+        }
+        if (live) live = __all_sync(0xffffffffu, bar_wait(&o_full[s], 0, &stop, p.err));
+        if (live) {
+            tc_after();
+            const float scale = l > 0.0f ? v_ref / l : (l == 0.0f ? 0.0f : l);
+            unsigned char* out = r < rows ? const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)) : nullptr;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t v[32];
+                tmem_load32(lanes + C::O_COL + s * D + c, v);
+                if (!out) continue;
+#pragma unroll
+                for (int e = 0; e < 32; e += 8) {
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = l == 0.0f ? 0.0f : __uint_as_float(v[e + i]) * scale;
+                    unsigned char* at = out + (c + e) * esize;
+                    if constexpr (PIECES == 2)
+                        store8(reinterpret_cast<float*>(at), x);
+                    else if (p.dtype == QG_DTYPE_F16)
+                        store8(reinterpret_cast<__half*>(at), x);
+                    else
+                        store8(reinterpret_cast<__nv_bfloat16*>(at), x);
+                }
+            }
+            if (p.lse && out) {
+                const int rr = (int)row0 + r;
+                p.lse[(long long)(sq.t0 + rr / p.group) * p.hq + h * p.group + rr % p.group] =
+                    l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945f;
+            }
+            tc_before();
+        }
+    } else if (warp >= 8 && warp < 12) {
+        // ================================ widening: codes to binary16 tiles
+        const int ct = tid - 256;
+        constexpr int KI = TN * D / 16 / 128;         // 16-byte pieces of K per thread
+        constexpr int VBLK = TN / 8 * (D / 16);       // V blocks of 8 tokens x 16 values
+        constexpr int VI = (VBLK + 127) / 128;
+        uint4 kr[KI], vr[VI][8];
+        auto load_k = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int e = i * 128 + ct, row = (e >> 2) % TN, db = (e >> 2) / TN;
+                bool ok;
+                const long long slot = slot_of(t_begin + j * TN + row, ok);
+                kr[i] = ldg_stream16(p.c.k + slot * D + db * 64 + (e & 3) * 16);
+            }
+        };
+        auto load_v = [&](int j) {
+#pragma unroll
+            for (int i = 0; i < VI; ++i) {
+                const int e = i * 128 + ct;
+                if (VBLK < 128 && e >= VBLK) break;
+                const int tg = e % (TN / 8), dg = e / (TN / 8), tok = t_begin + j * TN + tg * 8;
+                bool ok;
+                const long long slot = slot_of(tok, ok);
+                const uint8_t* at = p.c.v + slot * D + dg * 16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    // a slot that no row sees may hold anything, an 8-bit NaN too
+                    if (FMT == QG_KV8_E4M3 && (!ok || tok + k >= t_end || tok + k < lo_min))
+                        vr[i][k] = make_uint4(0, 0, 0, 0);
+                    else
+                        vr[i][k] = ldg_stream16(at + k * D);
+                }
+            }
+        };
+        load_k(0);
+        load_v(0);
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j % ST, phase = ((j / ST) & 1) ^ 1;
+            live = __all_sync(0xffffffffu, bar_wait(&k_empty[st], phase, &stop, p.err));
+            if (!live) break;
+            if (ct < TN / 16) {
+                const int tok = t_begin + j * TN + ct * 16;
+                bool ok;
+                const long long slot = slot_of(tok, ok);
+                const bool in = tok < t_end;
+                info[j & 3].ks[ct] = ok ? p.c.ks[slot >> p.c.block_log2] : 0.0f;
+                info[j & 3].u[ct] = ok ? p.c.vs[slot >> p.c.block_log2] * v_inv : 0.0f;
+                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, in && !ok);
+                if (ct == 0) info[j & 3].hidden = (int)hid;
+            }
+            unsigned char* kt = kst + st * C::K_BYTES;
+#pragma unroll
+            for (int i = 0; i < KI; ++i) {
+                const int e = i * 128 + ct, row = (e >> 2) % TN, db = (e >> 2) / TN;
+                uint4 a, z;
+                codes_to_half<FMT>(kr[i].x, a.x, a.y);
+                codes_to_half<FMT>(kr[i].y, a.z, a.w);
+                codes_to_half<FMT>(kr[i].z, z.x, z.y);
+                codes_to_half<FMT>(kr[i].w, z.z, z.w);
+                unsigned char* at = kt + db * (TN * 128) + row * 128;
+                const int c = (e & 3) * 2;
+                *reinterpret_cast<uint4*>(at + ((c ^ (row & 7)) << 4)) = a;
+                *reinterpret_cast<uint4*>(at + (((c + 1) ^ (row & 7)) << 4)) = z;
+            }
+            fence_async_smem();
+            bar_arrive(&k_full[st]);
+            if (j + 1 < tiles) load_k(j + 1);
+            live = __all_sync(0xffffffffu, bar_wait(&v_empty[st], phase, &stop, p.err));
+            if (!live) break;
+            unsigned char* vt_ = vst + st * C::K_BYTES;
+#pragma unroll
+            for (int i = 0; i < VI; ++i) {
+                const int e = i * 128 + ct;
+                if (VBLK < 128 && e >= VBLK) break;
+                const int tg = e % (TN / 8), dg = e / (TN / 8);
+                unsigned char* at = vt_ + (tg >> 3) * (D * 128);
+#pragma unroll
+                for (int wd = 0; wd < 4; ++wd) {
+                    uint32_t o[4][4];  // [value][token pair]
+#pragma unroll
+                    for (int tp = 0; tp < 4; ++tp) {
+                        const uint32_t a = reinterpret_cast<const uint32_t*>(&vr[i][2 * tp])[wd];
+                        const uint32_t z = reinterpret_cast<const uint32_t*>(&vr[i][2 * tp + 1])[wd];
+                        codes_to_half<FMT>(__byte_perm(a, z, 0x5140), o[0][tp], o[1][tp]);
+                        codes_to_half<FMT>(__byte_perm(a, z, 0x7362), o[2][tp], o[3][tp]);
+                    }
+#pragma unroll
+                    for (int f = 0; f < 4; ++f) {
+                        const int row = dg * 16 + wd * 4 + f;
+                        *reinterpret_cast<uint4*>(at + row * 128 + (((tg & 7) ^ (row & 7)) << 4)) =
+                            make_uint4(o[f][0], o[f][1], o[f][2], o[f][3]);
+                    }
+                }
+            }
+            fence_async_smem();
+            bar_arrive(&v_full[st]);
+            if (j + 1 < tiles) load_v(j + 1);
+        }
+    } else if (warp == 12) {
+        // ================================ one thread issues every matrix instruction
+        if (lane == 0) {
+            const uint32_t q0 = smem_addr(qs), k0 = smem_addr(kst), v0 = smem_addr(vst);
+            auto scores = [&](int s, int buf, int st) {
+                bool add = false;
+#pragma unroll
+                for (int pc = 0; pc < PIECES; ++pc)
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        mma_smem(tmem + buf * TN,
+                                 tile_desc(q0 + (s * PIECES + pc) * C::Q_BYTES + (k >> 2) * (PF_ROWS * 128) + (k & 3) * 32),
+                                 tile_desc(k0 + st * C::K_BYTES + (k >> 2) * (TN * 128) + (k & 3) * 32), mma_desc(TN), add);
+                        add = true;
+                    }
+            };
+            auto values = [&](int s, int buf, int st, bool add) {
+#pragma unroll
+                for (int pc = 0; pc < PIECES; ++pc)
+#pragma unroll
+                    for (int k = 0; k < TN / 16; ++k) {
+                        mma_tmem(tmem + C::O_COL + s * D, tmem + buf * TN + pc * (TN / 2) + k * 8,
+                                 tile_desc(v0 + st * C::K_BYTES + (k >> 2) * (D * 128) + (k & 3) * 32), mma_desc(D), add);
+                        add = true;
+                    }
+            };
+            // the products' completion, and this thread's own arrival: it has seen the tile's
+            // scales (k_full), so whoever waits here sees them too
+            auto scores_out = [&](uint64_t* bar) {
+                tc_commit(bar);
+                bar_arrive(bar);
+            };
+            auto wait = [&](uint64_t* bar, int phase) { return live = live && bar_wait(bar, phase & 1, &stop, p.err); };
+            if (wait(&k_full[0], 0)) {
+                tc_after();
+#pragma unroll 1
+                for (int s = 0; s < R; ++s) {
+                    scores(s, s, 0);
+                    scores_out(&s_full[s]);
+                }
+                tc_commit(&k_empty[0]);
+            }
+#pragma unroll 1
+            for (int j = 0; j < tiles && live; ++j) {
+                const int st = j % ST, nst = (j + 1) % ST;
+                if constexpr (R == 1) {
+                    if (j + 1 < tiles) {
+                        if (!wait(&k_full[nst], (j + 1) / ST)) break;
+                        tc_after();
+                        scores(0, (j + 1) & 1, nst);
+                        scores_out(&s_full[(j + 1) & 1]);
+                        tc_commit(&k_empty[nst]);
+                    }
+                    if (!wait(&v_full[st], j / ST) || !wait(&p_ready[j & 1], j >> 1)) break;
+                    tc_after();
+                    values(0, j & 1, st, j > 0);
+                    tc_commit(&pv_done);
+                    tc_commit(&v_empty[st]);
+                } else {
+                    if (!wait(&v_full[st], j / ST)) break;
+#pragma unroll 1
+                    for (int s = 0; s < R; ++s) {
+                        if (!wait(&p_ready[s], j)) break;
+                        tc_after();
+                        values(s, s, st, j > 0);
+                        if (s == R - 1) tc_commit(&v_empty[st]);
+                        if (j + 1 < tiles) {
+                            if (s == 0 && !wait(&k_full[nst], (j + 1) / ST)) break;
+                            tc_after();
+                            scores(s, s, nst);
+                            scores_out(&s_full[s]);
+                            if (s == R - 1) tc_commit(&k_empty[nst]);
+                        }
+                    }
+                }
+            }
+            if (live)
+                for (int s = 0; s < R; ++s) tc_commit(&o_full[s]);
+            // nothing may be in flight when TMEM is given back
+            tc_commit(&drained);
+            const unsigned long long t0 = globaltimer_ns();
+            while (!bar_try(&drained, 0) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
+            }
+        }
+        __syncwarp();
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+template <int D, int FMT, int PIECES>
+static int launch_shape(const AttnParams& p, const LaunchCtx& lc) {
+    using C = Prefill<D, PIECES>;
+    const void* kernel = reinterpret_cast<const void*>(prefill_kernel<D, FMT, PIECES>);
+    const int rc = ensure_smem_attr(kernel, C::smem, lc);
+    if (rc != QG_OK) return rc;
+    const long long tiles = (long long)p.tokens * p.group / (C::R * PF_ROWS) + p.c.batch;
+    if (tiles > 0x7fffffffll || p.c.hkv > 65535) return QG_ERR_UNSUPPORTED;
+    return launch_kernel(prefill_kernel<D, FMT, PIECES>, dim3((unsigned)tiles, (unsigned)p.c.hkv), dim3(PF_THREADS), C::smem, lc, p);
+}
+
+template <int FMT, int PIECES>
+static int launch_d(const AttnParams& p, int d, const LaunchCtx& lc) {
+    switch (d) {
+        case 64:
+            return launch_shape<64, FMT, PIECES>(p, lc);
+        case 128:
+            return launch_shape<128, FMT, PIECES>(p, lc);
+        default:
+            return launch_shape<256, FMT, PIECES>(p, lc);
+    }
+}
+
+int launch_prefill(const AttnParams& p, int format, int d, const LaunchCtx& lc) {
+    const bool f32 = p.dtype == QG_DTYPE_F32;
+    if (format == QG_KV8_INT8) return f32 ? launch_d<QG_KV8_INT8, 2>(p, d, lc) : launch_d<QG_KV8_INT8, 1>(p, d, lc);
+    return f32 ? launch_d<QG_KV8_E4M3, 2>(p, d, lc) : launch_d<QG_KV8_E4M3, 1>(p, d, lc);
+}
+
+}  // namespace kv8
+}  // namespace qg
