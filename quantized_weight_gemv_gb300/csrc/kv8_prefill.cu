@@ -77,6 +77,12 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
 }
+// true in one lane of the converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t yes;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(yes));
+    return yes != 0;
+}
 // K-major tile of 128-byte rows, 128-byte swizzle, 1024 bytes per group of eight rows
 __device__ __forceinline__ uint64_t tile_desc(uint32_t addr) {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
@@ -97,14 +103,22 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
 }
 #define QG_R8(v, o) "=r"(v[o]), "=r"(v[o + 1]), "=r"(v[o + 2]), "=r"(v[o + 3]), "=r"(v[o + 4]), "=r"(v[o + 5]), "=r"(v[o + 6]), "=r"(v[o + 7])
 #define QG_W8(v, o) "r"(v[o]), "r"(v[o + 1]), "r"(v[o + 2]), "r"(v[o + 3]), "r"(v[o + 4]), "r"(v[o + 5]), "r"(v[o + 6]), "r"(v[o + 7])
-// 32 columns of the warp's 32 lanes (a lane's row)
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+#define QG_X8(v, o) "+r"(v[o]), "+r"(v[o + 1]), "+r"(v[o + 2]), "+r"(v[o + 3]), "+r"(v[o + 4]), "+r"(v[o + 5]), "+r"(v[o + 6]), "+r"(v[o + 7])
+// 32 columns of the warp's 32 lanes (a lane's row): requested, then waited for
+__device__ __forceinline__ void tmem_request32(uint32_t at, uint32_t (&v)[32]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
-        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
+        "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
         : QG_R8(v, 0), QG_R8(v, 8), QG_R8(v, 16), QG_R8(v, 24)
         : "r"(at)
         : "memory");
+}
+__device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0), QG_X8(v, 8), QG_X8(v, 16), QG_X8(v, 24)::"memory");
+}
+__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
+    tmem_request32(at, v);
+    tmem_wait32(v);
 }
 __device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
     asm volatile(
@@ -129,6 +143,9 @@ struct TileInfo {
     int hidden;         // bit i: these 16 tokens could not be read
 };
 
+// the widening warpgroup's own barrier
+__device__ __forceinline__ void convert_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
 template <int D, int FMT, int PIECES>
 __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams p) {
     using C = Prefill<D, PIECES>;
@@ -136,6 +153,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], pv_done, drained;
     __shared__ TileInfo<TN> info[4];
+    __shared__ long long slots[2][TN / 16];  // the token slots of a tile's blocks of 16 (widening warpgroup)
     __shared__ float row_factor[RR];
     __shared__ unsigned v_top;  // the largest value scale, as bits
     __shared__ int stop;
@@ -309,36 +327,44 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             const int tok = t_begin + j * TN;
             const int hidden = ti.hidden;
             const bool plain = !cap && !hidden && tok + TN - 1 <= hi_min && tok >= lo_max;
-            // the score of column c (its raw product v) in base 2
-            auto score = [&](float v, int c) {
-                float x = v * (rf * ti.ks[c >> 4]);
-                if (cap) x = cap2 * tanhf(x);
-                const int t = tok + c;
-                return t > hi || t < lo || ((hidden >> (c >> 4)) & 1) ? -INFINITY : x;
+            // products v of columns c.. as scores in base 2, where the plain factor is not all there is to it
+            auto to_scores = [&](uint32_t (&v)[32], int c) {
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const float f = rf * ti.ks[c / 16 + q];
+                    const bool hid = (hidden >> (c / 16 + q)) & 1;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float x = __uint_as_float(v[16 * q + e]) * f;
+                        if (cap) x = cap2 * tanhf(x);
+                        const int t = tok + c + 16 * q + e;
+                        v[16 * q + e] = __float_as_uint(t > hi || t < lo || hid ? -INFINITY : x);
+                    }
+                }
             };
+            auto factor = [&](int block) { return plain ? rf * ti.ks[block] : 1.0f; };
             // the largest score, to see whether the reference holds
             float m = -INFINITY;
             uint32_t hold[PIECES == 2 ? TN / 2 : 1];  // two pieces of P cover all of S: its upper half is kept
+            uint32_t v[2][32];
+            tmem_request32(st, v[0]);
 #pragma unroll
             for (int c = 0; c < TN; c += 32) {
-                uint32_t v[32];
-                tmem_load32(st + c, v);
-                if (plain) {
+                uint32_t(&x)[32] = v[(c / 32) & 1];
+                tmem_wait32(x);
+                tmem_request32(st + (c + 32 < TN ? c + 32 : 0), v[(c / 32 + 1) & 1]);  // last: the weights' first
+                if (!plain) to_scores(x, c);
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        float x = __uint_as_float(v[16 * q]);
+                for (int q = 0; q < 2; ++q) {
+                    float y = __uint_as_float(x[16 * q]);
 #pragma unroll
-                        for (int e = 1; e < 16; ++e) x = fmaxf(x, __uint_as_float(v[16 * q + e]));
-                        m = fmaxf(m, x * (rf * ti.ks[c / 16 + q]));
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) m = fmaxf(m, score(__uint_as_float(v[e]), c + e));
+                    for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * q + e]));
+                    m = fmaxf(m, y * factor(c / 16 + q));
                 }
                 if constexpr (PIECES == 2)
                     if (c >= TN / 2) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) hold[c - TN / 2 + e] = v[e];
+                        for (int e = 0; e < 32; ++e) hold[c - TN / 2 + e] = x[e];
                     }
             }
             if (__any_sync(0xffffffffu, m > mo + (P_BITS + P_SLACK))) {
@@ -348,50 +374,37 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 if (j > 0) {
                     if (R == 1) {  // the last product may still be running
                         live = __all_sync(0xffffffffu, bar_wait(&pv_done, (j - 1) & 1, &stop, p.err));
+                        tmem_wait32(v[0]);
                         if (!live) break;
                         tc_after();
                     }
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
-                        uint32_t v[32];
-                        tmem_load32(lanes + C::O_COL + s * D + c, v);
+                        uint32_t o[32];
+                        tmem_load32(lanes + C::O_COL + s * D + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-                        tmem_store32(lanes + C::O_COL + s * D + c, v);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        tmem_store32(lanes + C::O_COL + s * D + c, o);
                     }
                 }
             }
-            // weights
-#pragma unroll
-            for (int c = 0; c < TN; c += 32) {
-                uint32_t v[32];
-                if (PIECES == 1 || c < TN / 2) {
-                    tmem_load32(st + c, v);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = hold[PIECES == 2 ? c - TN / 2 + e : 0];
-                }
+            // weights (TN / 32 is even: the first columns are in v[0] again)
+            auto weights = [&](const uint32_t (&x)[32], int c, bool select) {
                 uint32_t w[16], w2[16];
                 float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const float f = rf * ti.ks[c / 16 + q], u = ti.u[c / 16 + q];
+                    const float f = factor(c / 16 + q), u = ti.u[c / 16 + q];
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         const int i = 16 * q + e;
-                        float a, z;
-                        if (plain) {
-                            a = ex2(fmaf(__uint_as_float(v[i]), f, -mo));
-                            z = ex2(fmaf(__uint_as_float(v[i + 1]), f, -mo));
-                        } else {
-                            a = ex2(score(__uint_as_float(v[i]), c + i) - mo);
-                            z = ex2(score(__uint_as_float(v[i + 1]), c + i + 1) - mo);
-                        }
+                        float a = ex2(fmaf(__uint_as_float(x[i]), f, -mo));
+                        float z = ex2(fmaf(__uint_as_float(x[i + 1]), f, -mo));
                         l4[e & 2] += a;
                         l4[(e & 2) + 1] += z;
                         // a hidden token's weight is 0 whatever its block's scale holds
-                        a = !plain && a == 0.0f ? 0.0f : a * u;
-                        z = !plain && z == 0.0f ? 0.0f : z * u;
+                        a = select && a == 0.0f ? 0.0f : a * u;
+                        z = select && z == 0.0f ? 0.0f : z * u;
                         const __half2 hi2 = __floats2half2_rn(a, z);
                         w[i / 2] = *reinterpret_cast<const uint32_t*>(&hi2);
                         if constexpr (PIECES == 2) w2[i / 2] = half2_bits(a - __low2float(hi2), z - __high2float(hi2));
@@ -400,6 +413,23 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
                 tmem_store16(st + c / 2, w);
                 if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + c / 2, w2);
+            };
+            constexpr int AGAIN = PIECES == 2 ? TN / 2 : TN;  // columns that are read again
+#pragma unroll
+            for (int c = 0; c < TN; c += 32) {
+                uint32_t(&x)[32] = v[(c / 32) & 1];
+                if (c < AGAIN) {
+                    tmem_wait32(x);
+                    if (c + 32 < AGAIN) tmem_request32(st + c + 32, v[(c / 32 + 1) & 1]);
+                    if (!plain) to_scores(x, c);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) x[e] = hold[PIECES == 2 ? c - TN / 2 + e : 0];
+                }
+                if (plain)
+                    weights(x, c, false);
+                else
+                    weights(x, c, true);
             }
             tmem_store_wait();
             tc_before();
@@ -443,13 +473,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         constexpr int VBLK = TN / 8 * (D / 16);       // V blocks of 8 tokens x 16 values
         constexpr int VI = (VBLK + 127) / 128;
         uint4 kr[KI], vr[VI][8];
+        // tile j's slots, and what the softmax needs of it; then barrier
+        auto look_up = [&](int j) {
+            if (ct < TN / 16) {
+                const int tok = t_begin + j * TN + ct * 16;
+                bool ok;
+                const long long slot = slot_of(tok, ok);
+                TileInfo<TN>& ti = info[j & 3];
+                slots[j & 1][ct] = slot;
+                ti.ks[ct] = ok ? p.c.ks[slot >> p.c.block_log2] : 0.0f;
+                ti.u[ct] = ok ? p.c.vs[slot >> p.c.block_log2] * v_inv : 0.0f;
+                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, tok < t_end && !ok);
+                if (ct == 0) ti.hidden = (int)hid;
+            }
+            convert_sync();
+        };
         auto load_k = [&](int j) {
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 const int e = i * 128 + ct, row = (e >> 2) % TN, db = (e >> 2) / TN;
-                bool ok;
-                const long long slot = slot_of(t_begin + j * TN + row, ok);
-                kr[i] = ldg_stream16(p.c.k + slot * D + db * 64 + (e & 3) * 16);
+                kr[i] = ldg_stream16(p.c.k + (slots[j & 1][row >> 4] + (row & 15)) * D + db * 64 + (e & 3) * 16);
             }
         };
         auto load_v = [&](int j) {
@@ -458,35 +501,26 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 const int e = i * 128 + ct;
                 if (VBLK < 128 && e >= VBLK) break;
                 const int tg = e % (TN / 8), dg = e / (TN / 8), tok = t_begin + j * TN + tg * 8;
-                bool ok;
-                const long long slot = slot_of(tok, ok);
-                const uint8_t* at = p.c.v + slot * D + dg * 16;
+                const uint8_t* at = p.c.v + (slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 16;
+                // slots that no row sees may hold anything, an 8-bit NaN too
+                const bool edge = FMT == QG_KV8_E4M3 && (tok + 8 > t_end || tok < lo_min || ((info[j & 3].hidden >> (tg >> 1)) & 1));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    // a slot that no row sees may hold anything, an 8-bit NaN too
-                    if (FMT == QG_KV8_E4M3 && (!ok || tok + k >= t_end || tok + k < lo_min))
-                        vr[i][k] = make_uint4(0, 0, 0, 0);
-                    else
-                        vr[i][k] = ldg_stream16(at + k * D);
+                for (int k = 0; k < 8; ++k) vr[i][k] = ldg_stream16(at + k * D);
+                if (edge) {
+                    const bool all = (info[j & 3].hidden >> (tg >> 1)) & 1;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (all || tok + k >= t_end || tok + k < lo_min) vr[i][k] = make_uint4(0, 0, 0, 0);
                 }
             }
         };
+        look_up(0);
         load_k(0);
         load_v(0);
         for (int j = 0; j < tiles; ++j) {
             const int st = j % ST, phase = ((j / ST) & 1) ^ 1;
             live = __all_sync(0xffffffffu, bar_wait(&k_empty[st], phase, &stop, p.err));
             if (!live) break;
-            if (ct < TN / 16) {
-                const int tok = t_begin + j * TN + ct * 16;
-                bool ok;
-                const long long slot = slot_of(tok, ok);
-                const bool in = tok < t_end;
-                info[j & 3].ks[ct] = ok ? p.c.ks[slot >> p.c.block_log2] : 0.0f;
-                info[j & 3].u[ct] = ok ? p.c.vs[slot >> p.c.block_log2] * v_inv : 0.0f;
-                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, in && !ok);
-                if (ct == 0) info[j & 3].hidden = (int)hid;
-            }
             unsigned char* kt = kst + st * C::K_BYTES;
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
@@ -503,7 +537,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             }
             fence_async_smem();
             bar_arrive(&k_full[st]);
-            if (j + 1 < tiles) load_k(j + 1);
+            if (j + 1 < tiles) {
+                look_up(j + 1);
+                load_k(j + 1);
+            }
             live = __all_sync(0xffffffffu, bar_wait(&v_empty[st], phase, &stop, p.err));
             if (!live) break;
             unsigned char* vt_ = vst + st * C::K_BYTES;
@@ -536,38 +573,48 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             if (j + 1 < tiles) load_v(j + 1);
         }
     } else if (warp == 12) {
-        // ================================ one thread issues every matrix instruction
-        if (lane == 0) {
+        // ================================ the matrix instructions: the warp runs as one, a lane issues
+        // (descriptors are then warp-uniform; issued from a divergent branch an instruction took
+        // over 100 cycles to set up)
+        {
+            const bool leader = elect_one();
             const uint32_t q0 = smem_addr(qs), k0 = smem_addr(kst), v0 = smem_addr(vst);
             auto scores = [&](int s, int buf, int st) {
-                bool add = false;
+                const uint32_t a0 = q0 + s * PIECES * C::Q_BYTES, b0 = k0 + st * C::K_BYTES;
+                if (leader) {
 #pragma unroll
-                for (int pc = 0; pc < PIECES; ++pc)
-#pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        mma_smem(tmem + buf * TN,
-                                 tile_desc(q0 + (s * PIECES + pc) * C::Q_BYTES + (k >> 2) * (PF_ROWS * 128) + (k & 3) * 32),
-                                 tile_desc(k0 + st * C::K_BYTES + (k >> 2) * (TN * 128) + (k & 3) * 32), mma_desc(TN), add);
-                        add = true;
+                    for (int i = 0; i < PIECES * D / 16; ++i) {
+                        const int pc = i / (D / 16), k = i % (D / 16);
+                        mma_smem(tmem + buf * TN, tile_desc(a0 + pc * C::Q_BYTES + (k >> 2) * (PF_ROWS * 128) + (k & 3) * 32),
+                                 tile_desc(b0 + (k >> 2) * (TN * 128) + (k & 3) * 32), mma_desc(TN), i > 0);
                     }
+                }
             };
             auto values = [&](int s, int buf, int st, bool add) {
+                const uint32_t b0 = v0 + st * C::K_BYTES;
+                if (leader) {
 #pragma unroll
-                for (int pc = 0; pc < PIECES; ++pc)
-#pragma unroll
-                    for (int k = 0; k < TN / 16; ++k) {
+                    for (int i = 0; i < PIECES * TN / 16; ++i) {
+                        const int pc = i / (TN / 16), k = i % (TN / 16);
                         mma_tmem(tmem + C::O_COL + s * D, tmem + buf * TN + pc * (TN / 2) + k * 8,
-                                 tile_desc(v0 + st * C::K_BYTES + (k >> 2) * (D * 128) + (k & 3) * 32), mma_desc(D), add);
-                        add = true;
+                                 tile_desc(b0 + (k >> 2) * (D * 128) + (k & 3) * 32), mma_desc(D), add || i > 0);
                     }
+                }
             };
             // the products' completion, and this thread's own arrival: it has seen the tile's
             // scales (k_full), so whoever waits here sees them too
             auto scores_out = [&](uint64_t* bar) {
-                tc_commit(bar);
-                bar_arrive(bar);
+                if (leader) {
+                    tc_commit(bar);
+                    bar_arrive(bar);
+                }
             };
-            auto wait = [&](uint64_t* bar, int phase) { return live = live && bar_wait(bar, phase & 1, &stop, p.err); };
+            auto commit = [&](uint64_t* bar) {
+                if (leader) tc_commit(bar);
+            };
+            auto wait = [&](uint64_t* bar, int phase) {
+                return live = live && __all_sync(0xffffffffu, bar_wait(bar, phase & 1, &stop, p.err));
+            };
             if (wait(&k_full[0], 0)) {
                 tc_after();
 #pragma unroll 1
@@ -575,7 +622,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                     scores(s, s, 0);
                     scores_out(&s_full[s]);
                 }
-                tc_commit(&k_empty[0]);
+                commit(&k_empty[0]);
             }
 #pragma unroll 1
             for (int j = 0; j < tiles && live; ++j) {
@@ -586,13 +633,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                         tc_after();
                         scores(0, (j + 1) & 1, nst);
                         scores_out(&s_full[(j + 1) & 1]);
-                        tc_commit(&k_empty[nst]);
+                        commit(&k_empty[nst]);
                     }
                     if (!wait(&v_full[st], j / ST) || !wait(&p_ready[j & 1], j >> 1)) break;
                     tc_after();
                     values(0, j & 1, st, j > 0);
-                    tc_commit(&pv_done);
-                    tc_commit(&v_empty[st]);
+                    commit(&pv_done);
+                    commit(&v_empty[st]);
                 } else {
                     if (!wait(&v_full[st], j / ST)) break;
 #pragma unroll 1
@@ -600,21 +647,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                         if (!wait(&p_ready[s], j)) break;
                         tc_after();
                         values(s, s, st, j > 0);
-                        if (s == R - 1) tc_commit(&v_empty[st]);
+                        if (s == R - 1) commit(&v_empty[st]);
                         if (j + 1 < tiles) {
                             if (s == 0 && !wait(&k_full[nst], (j + 1) / ST)) break;
                             tc_after();
                             scores(s, s, nst);
                             scores_out(&s_full[s]);
-                            if (s == R - 1) tc_commit(&k_empty[nst]);
+                            if (s == R - 1) commit(&k_empty[nst]);
                         }
                     }
                 }
             }
             if (live)
-                for (int s = 0; s < R; ++s) tc_commit(&o_full[s]);
+                for (int s = 0; s < R; ++s) commit(&o_full[s]);
             // nothing may be in flight when TMEM is given back
-            tc_commit(&drained);
+            commit(&drained);
             const unsigned long long t0 = globaltimer_ns();
             while (!bar_try(&drained, 0) && globaltimer_ns() - t0 < WAIT_LIMIT_NS) {
             }
