@@ -13,9 +13,9 @@
 // Roles (13 warps): one warpgroup per row tile does the softmax, a thread per row; one
 // warpgroup widens the next tile's codes from registers into the 128-byte-swizzled K-major
 // tiles that the matrix instructions read (V transposed on the way: pairs of tokens are
-// interleaved by byte permutes); one thread issues.  R = 2 row tiles (D <= 128) keep the
-// tensor cores on one tile while the other's softmax runs; at D = 256 TMEM holds one row
-// tile and S is double-buffered instead.
+// interleaved by byte permutes); one warp issues.  S is double-buffered, so the scores of
+// the next tile are ready when a row tile's softmax has finished this one; R = 2 row tiles
+// (D <= 128, all of TMEM) share each widened tile, at D = 256 one fits.
 // The softmax reference m moves only when a score leaves it by more than 2^4; O is then
 // rescaled in TMEM by the row's own thread.  Every wait is bounded.
 #include "kv8.cuh"
@@ -29,13 +29,13 @@ constexpr int PF_ROWS = 128;  // rows of one matrix instruction
 template <int D, int PIECES>
 struct Prefill {
     static constexpr int R = D == 256 ? 1 : 2;            // row tiles per CTA
-    static constexpr int TN = D == 256 ? 64 : 128;        // cache tokens per tile
-    static constexpr int ST = PIECES == 2 && D >= 128 ? 1 : 2;  // K and V buffers
+    static constexpr int TN = 64;                         // cache tokens per tile
+    static constexpr int ST = PIECES == 2 && D == 256 ? 1 : 2;  // K and V buffers
     static constexpr int Q_BYTES = PF_ROWS * D * 2;       // one piece of one row tile
     static constexpr int K_BYTES = TN * D * 2;
     static constexpr int used = R * PIECES * Q_BYTES + ST * 2 * K_BYTES + 1024;
     static constexpr int smem = used > 120 * 1024 ? used : 120 * 1024;  // one CTA per SM: each takes all of TMEM
-    static constexpr int O_COL = 2 * TN;                  // TMEM: two S buffers, then R outputs
+    static constexpr int O_COL = 256;                     // TMEM: two S buffers per row tile, then the outputs
     static_assert(O_COL + R * D <= 512, "TMEM columns");
     static_assert(smem <= 227 * 1024, "shared memory");
 };
@@ -51,15 +51,14 @@ __device__ __forceinline__ void bar_arrive(uint64_t* b) {
 __device__ __forceinline__ bool bar_try(uint64_t* b, unsigned parity) {
     uint32_t ok;
     asm volatile(
-        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_addr(b)), "r"(parity)
+        : "r"(smem_addr(b)), "r"(parity), "r"(20000u)  // suspended for up to 20 us at a time
         : "memory");
     return ok != 0;
 }
 // false once the wait has run out here or anywhere in the CTA
-__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
-    if (bar_try(b, parity)) return true;
+__device__ __noinline__ bool bar_wait_slow(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
     const unsigned long long t0 = globaltimer_ns();
     while (!bar_try(b, parity)) {
         if (*stop) return false;
@@ -70,6 +69,10 @@ __device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile 
         }
     }
     return true;
+}
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
+    if (bar_try(b, parity)) return true;
+    return bar_wait_slow(b, parity, stop, err);
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -113,18 +116,45 @@ __device__ __forceinline__ void tmem_request32(uint32_t at, uint32_t (&v)[32]) {
         : "r"(at)
         : "memory");
 }
+__device__ __forceinline__ void tmem_wait64(uint32_t (&v)[32], uint32_t (&z)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0), QG_X8(v, 8), QG_X8(v, 16), QG_X8(v, 24)::"memory");
+    asm volatile("" : QG_X8(z, 0), QG_X8(z, 8), QG_X8(z, 16), QG_X8(z, 24)::"memory");
+}
 __device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0), QG_X8(v, 8), QG_X8(v, 16), QG_X8(v, 24)::"memory");
+}
+// two fp32 lanes of one register pair
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    return (unsigned long long)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float2 unpair(unsigned long long v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 __device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
     tmem_request32(at, v);
     tmem_wait32(v);
 }
-__device__ __forceinline__ void tmem_store32(uint32_t at, const uint32_t (&v)[32]) {
+__device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
-        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::QG_W8(v, 0),
-        QG_W8(v, 8), QG_W8(v, 16), QG_W8(v, 24), "r"(at)
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : QG_R8(v, 0), QG_R8(v, 8)
+        : "r"(at)
         : "memory");
 }
 __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16]) {
@@ -151,7 +181,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     using C = Prefill<D, PIECES>;
     constexpr int R = C::R, TN = C::TN, ST = C::ST, RR = R * PF_ROWS;
     extern __shared__ unsigned char smem_raw[];
-    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], o_full[2], pv_done, drained;
+    __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], o_full[2], pv_done[2], drained;
+    __shared__ uint64_t s_full[2][2], p_ready[2][2];  // [row tile][S buffer]
     __shared__ TileInfo<TN> info[4];
     __shared__ long long slots[2][TN / 16];  // the token slots of a tile's blocks of 16 (widening warpgroup)
     __shared__ float row_factor[RR];
@@ -212,11 +243,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             bar_init(&v_full[i], 128);
             bar_init(&k_empty[i], 1);
             bar_init(&v_empty[i], 1);
-            bar_init(&s_full[i], 2);
-            bar_init(&p_ready[i], 128);
+            for (int k = 0; k < 2; ++k) {
+                bar_init(&s_full[i][k], 2);
+                bar_init(&p_ready[i][k], 128);
+            }
             bar_init(&o_full[i], 1);
+            bar_init(&pv_done[i], 1);
         }
-        bar_init(&pv_done, 1);
         bar_init(&drained, 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         v_top = 0u;
@@ -316,129 +349,101 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         }
         const float cap2 = p.softcap * 1.44269504088896f;
         const bool cap = p.softcap > 0.0f;
-        float mo = -1e30f, l = 0.0f;
+        float mo = -1e30f;
+        unsigned long long l = 0ull;  // two sums
         for (int j = 0; j < tiles && live; ++j) {
-            const int buf = R == 2 ? s : j & 1, phase = R == 2 ? j & 1 : (j >> 1) & 1;
-            live = __all_sync(0xffffffffu, bar_wait(&s_full[buf], phase, &stop, p.err));
+            const int buf = j & 1, phase = (j >> 1) & 1;
+            live = __all_sync(0xffffffffu, bar_wait(&s_full[s][buf], phase, &stop, p.err));
             if (!live) break;
             tc_after();
+            const uint32_t st = lanes + (2 * s + buf) * TN;
+            uint32_t v[2][32];
+            tmem_request32(st, v[0]);
+            tmem_request32(st + 32, v[1]);
             const TileInfo<TN>& ti = info[j & 3];
-            const uint32_t st = lanes + buf * TN;
             const int tok = t_begin + j * TN;
             const int hidden = ti.hidden;
             const bool plain = !cap && !hidden && tok + TN - 1 <= hi_min && tok >= lo_max;
-            // products v of columns c.. as scores in base 2, where the plain factor is not all there is to it
-            auto to_scores = [&](uint32_t (&v)[32], int c) {
+            float f[TN / 16], u[TN / 16];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float f = rf * ti.ks[c / 16 + q];
-                    const bool hid = (hidden >> (c / 16 + q)) & 1;
+            for (int i = 0; i < TN / 16; ++i) {
+                f[i] = rf * ti.ks[i];
+                u[i] = ti.u[i];
+            }
+            tmem_wait64(v[0], v[1]);
+            if (!plain) {  // products as scores in base 2, with the cap and the mask
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        float x = __uint_as_float(v[16 * q + e]) * f;
-                        if (cap) x = cap2 * tanhf(x);
-                        const int t = tok + c + 16 * q + e;
-                        v[16 * q + e] = __float_as_uint(t > hi || t < lo || hid ? -INFINITY : x);
-                    }
+                for (int i = 0; i < TN; ++i) {
+                    uint32_t& r_ = v[i >> 5][i & 31];
+                    float x = __uint_as_float(r_) * f[i >> 4];
+                    if (cap) x = cap2 * tanhf(x);
+                    const int t = tok + i;
+                    r_ = __float_as_uint(t > hi || t < lo || ((hidden >> (i >> 4)) & 1) ? -INFINITY : x);
                 }
-            };
-            auto factor = [&](int block) { return plain ? rf * ti.ks[block] : 1.0f; };
+#pragma unroll
+                for (int i = 0; i < TN / 16; ++i) f[i] = 1.0f;
+            }
             // the largest score, to see whether the reference holds
             float m = -INFINITY;
-            uint32_t hold[PIECES == 2 ? TN / 2 : 1];  // two pieces of P cover all of S: its upper half is kept
-            uint32_t v[2][32];
-            tmem_request32(st, v[0]);
 #pragma unroll
-            for (int c = 0; c < TN; c += 32) {
-                uint32_t(&x)[32] = v[(c / 32) & 1];
-                tmem_wait32(x);
-                tmem_request32(st + (c + 32 < TN ? c + 32 : 0), v[(c / 32 + 1) & 1]);  // last: the weights' first
-                if (!plain) to_scores(x, c);
+            for (int q = 0; q < TN / 16; ++q) {
+                float y = __uint_as_float(v[q >> 1][16 * (q & 1)]);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    float y = __uint_as_float(x[16 * q]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(x[16 * q + e]));
-                    m = fmaxf(m, y * factor(c / 16 + q));
-                }
-                if constexpr (PIECES == 2)
-                    if (c >= TN / 2) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) hold[c - TN / 2 + e] = x[e];
-                    }
+                for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(v[q >> 1][16 * (q & 1) + e]));
+                m = fmaxf(m, y * f[q]);
             }
             if (__any_sync(0xffffffffu, m > mo + (P_BITS + P_SLACK))) {
-                const float to = fmaxf(mo, m - P_BITS), f = ex2(mo - to);
-                l *= f;
+                const float to = fmaxf(mo, m - P_BITS), by = ex2(mo - to);
+                l = mul2(l, pair(by, by));
                 mo = to;
-                if (j > 0) {
-                    if (R == 1) {  // the last product may still be running
-                        live = __all_sync(0xffffffffu, bar_wait(&pv_done, (j - 1) & 1, &stop, p.err));
-                        tmem_wait32(v[0]);
-                        if (!live) break;
-                        tc_after();
-                    }
+                if (j > 0) {  // the last product may still be running
+                    live = __all_sync(0xffffffffu, bar_wait(&pv_done[s], (j - 1) & 1, &stop, p.err));
+                    if (!live) break;
+                    tc_after();
 #pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t o[32];
-                        tmem_load32(lanes + C::O_COL + s * D + c, o);
+                    for (int c = 0; c < D; c += 16) {
+                        uint32_t o[16];
+                        tmem_load16(lanes + C::O_COL + s * D + c, o);
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        tmem_store32(lanes + C::O_COL + s * D + c, o);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * by);
+                        tmem_store16(lanes + C::O_COL + s * D + c, o);
                     }
                 }
             }
-            // weights (TN / 32 is even: the first columns are in v[0] again)
-            auto weights = [&](const uint32_t (&x)[32], int c, bool select) {
+            // weights; a hidden token's is 0 whatever its block's scale holds
+            const unsigned long long mo2 = pair(-mo, -mo);
+#pragma unroll
+            for (int q = 0; q < TN / 32; ++q) {
                 uint32_t w[16], w2[16];
-                float l4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const float f = factor(c / 16 + q), u = ti.u[c / 16 + q];
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const int i = 16 * q + e;
-                        float a = ex2(fmaf(__uint_as_float(x[i]), f, -mo));
-                        float z = ex2(fmaf(__uint_as_float(x[i + 1]), f, -mo));
-                        l4[e & 2] += a;
-                        l4[(e & 2) + 1] += z;
-                        // a hidden token's weight is 0 whatever its block's scale holds
-                        a = select && a == 0.0f ? 0.0f : a * u;
-                        z = select && z == 0.0f ? 0.0f : z * u;
-                        const __half2 hi2 = __floats2half2_rn(a, z);
-                        w[i / 2] = *reinterpret_cast<const uint32_t*>(&hi2);
-                        if constexpr (PIECES == 2) w2[i / 2] = half2_bits(a - __low2float(hi2), z - __high2float(hi2));
+                for (int e = 0; e < 32; e += 2) {
+                    const int i = 32 * q + e;
+                    const float fi = f[i >> 4], ui = u[i >> 4];
+                    const float2 x = unpair(fma2(pair(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), pair(fi, fi), mo2));
+                    const unsigned long long pp = pair(ex2(x.x), ex2(x.y));
+                    l = add2(l, pp);
+                    float2 a = unpair(mul2(pp, pair(ui, ui)));
+                    if (!plain) {
+                        const float2 z = unpair(pp);
+                        if (z.x == 0.0f) a.x = 0.0f;
+                        if (z.y == 0.0f) a.y = 0.0f;
                     }
+                    const __half2 hi2 = __floats2half2_rn(a.x, a.y);
+                    w[e / 2] = *reinterpret_cast<const uint32_t*>(&hi2);
+                    if constexpr (PIECES == 2) w2[e / 2] = half2_bits(a.x - __low2float(hi2), a.y - __high2float(hi2));
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-                tmem_store16(st + c / 2, w);
-                if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + c / 2, w2);
-            };
-            constexpr int AGAIN = PIECES == 2 ? TN / 2 : TN;  // columns that are read again
-#pragma unroll
-            for (int c = 0; c < TN; c += 32) {
-                uint32_t(&x)[32] = v[(c / 32) & 1];
-                if (c < AGAIN) {
-                    tmem_wait32(x);
-                    if (c + 32 < AGAIN) tmem_request32(st + c + 32, v[(c / 32 + 1) & 1]);
-                    if (!plain) to_scores(x, c);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[e] = hold[PIECES == 2 ? c - TN / 2 + e : 0];
-                }
-                if (plain)
-                    weights(x, c, false);
-                else
-                    weights(x, c, true);
+                tmem_store16(st + 16 * q, w);
+                if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + 16 * q, w2);
             }
             tmem_store_wait();
             tc_before();
-            bar_arrive(&p_ready[buf]);
+            bar_arrive(&p_ready[s][buf]);
         }
         if (live) live = __all_sync(0xffffffffu, bar_wait(&o_full[s], 0, &stop, p.err));
         if (live) {
             tc_after();
-            const float scale = l > 0.0f ? v_ref / l : (l == 0.0f ? 0.0f : l);
+            const float sum = unpair(l).x + unpair(l).y;
+            const float scale = sum > 0.0f ? v_ref / sum : (sum == 0.0f ? 0.0f : sum);
             unsigned char* out = r < rows ? const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)) : nullptr;
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -449,7 +454,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 for (int e = 0; e < 32; e += 8) {
                     float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = l == 0.0f ? 0.0f : __uint_as_float(v[e + i]) * scale;
+                    for (int i = 0; i < 8; ++i) x[i] = sum == 0.0f ? 0.0f : __uint_as_float(v[e + i]) * scale;
                     unsigned char* at = out + (c + e) * esize;
                     if constexpr (PIECES == 2)
                         store8(reinterpret_cast<float*>(at), x);
@@ -462,7 +467,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             if (p.lse && out) {
                 const int rr = (int)row0 + r;
                 p.lse[(long long)(sq.t0 + rr / p.group) * p.hq + h * p.group + rr % p.group] =
-                    l == 0.0f ? -INFINITY : (mo + log2f(l)) * 0.693147180559945f;
+                    sum == 0.0f ? -INFINITY : (mo + log2f(sum)) * 0.693147180559945f;
             }
             tc_before();
         }
@@ -470,20 +475,29 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         // ================================ widening: codes to binary16 tiles
         const int ct = tid - 256;
         constexpr int KI = TN * D / 16 / 128;         // 16-byte pieces of K per thread
-        constexpr int VBLK = TN / 8 * (D / 16);       // V blocks of 8 tokens x 16 values
+        constexpr int VBLK = TN / 8 * (D / 8);        // V blocks of 8 tokens x 8 values
         constexpr int VI = (VBLK + 127) / 128;
-        uint4 kr[KI], vr[VI][8];
-        // tile j's slots, and what the softmax needs of it; then barrier
-        auto look_up = [&](int j) {
+        uint4 kr[KI];
+        uint2 vr[VI][8];
+        // A tile's slots, and what the softmax needs of it, are requested a tile ahead (by the
+        // first TN / 16 threads) and published at a barrier.
+        long long next_slot = 0;
+        float next_ks = 0.0f, next_u = 0.0f;
+        bool next_ok = false;
+        auto request = [&](int j) {
             if (ct < TN / 16) {
-                const int tok = t_begin + j * TN + ct * 16;
-                bool ok;
-                const long long slot = slot_of(tok, ok);
+                next_slot = slot_of(t_begin + j * TN + ct * 16, next_ok);
+                next_ks = p.c.ks[next_slot >> p.c.block_log2];
+                next_u = p.c.vs[next_slot >> p.c.block_log2];
+            }
+        };
+        auto publish = [&](int j) {
+            if (ct < TN / 16) {
                 TileInfo<TN>& ti = info[j & 3];
-                slots[j & 1][ct] = slot;
-                ti.ks[ct] = ok ? p.c.ks[slot >> p.c.block_log2] : 0.0f;
-                ti.u[ct] = ok ? p.c.vs[slot >> p.c.block_log2] * v_inv : 0.0f;
-                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, tok < t_end && !ok);
+                slots[j & 1][ct] = next_slot;
+                ti.ks[ct] = next_ok ? next_ks : 0.0f;
+                ti.u[ct] = next_ok ? next_u * v_inv : 0.0f;
+                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, t_begin + j * TN + ct * 16 < t_end && !next_ok);
                 if (ct == 0) ti.hidden = (int)hid;
             }
             convert_sync();
@@ -501,20 +515,22 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 const int e = i * 128 + ct;
                 if (VBLK < 128 && e >= VBLK) break;
                 const int tg = e % (TN / 8), dg = e / (TN / 8), tok = t_begin + j * TN + tg * 8;
-                const uint8_t* at = p.c.v + (slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 16;
+                const uint8_t* at = p.c.v + (slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 8;
                 // slots that no row sees may hold anything, an 8-bit NaN too
                 const bool edge = FMT == QG_KV8_E4M3 && (tok + 8 > t_end || tok < lo_min || ((info[j & 3].hidden >> (tg >> 1)) & 1));
 #pragma unroll
-                for (int k = 0; k < 8; ++k) vr[i][k] = ldg_stream16(at + k * D);
+                for (int k = 0; k < 8; ++k) vr[i][k] = ldg_stream8(at + k * D);
                 if (edge) {
                     const bool all = (info[j & 3].hidden >> (tg >> 1)) & 1;
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        if (all || tok + k >= t_end || tok + k < lo_min) vr[i][k] = make_uint4(0, 0, 0, 0);
+                        if (all || tok + k >= t_end || tok + k < lo_min) vr[i][k] = make_uint2(0u, 0u);
                 }
             }
         };
-        look_up(0);
+        request(0);
+        publish(0);
+        request(1);
         load_k(0);
         load_v(0);
         for (int j = 0; j < tiles; ++j) {
@@ -538,8 +554,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             fence_async_smem();
             bar_arrive(&k_full[st]);
             if (j + 1 < tiles) {
-                look_up(j + 1);
+                publish(j + 1);
                 load_k(j + 1);
+                request(j + 2);
             }
             live = __all_sync(0xffffffffu, bar_wait(&v_empty[st], phase, &stop, p.err));
             if (!live) break;
@@ -551,7 +568,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 const int tg = e % (TN / 8), dg = e / (TN / 8);
                 unsigned char* at = vt_ + (tg >> 3) * (D * 128);
 #pragma unroll
-                for (int wd = 0; wd < 4; ++wd) {
+                for (int wd = 0; wd < 2; ++wd) {
                     uint32_t o[4][4];  // [value][token pair]
 #pragma unroll
                     for (int tp = 0; tp < 4; ++tp) {
@@ -562,7 +579,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                     }
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
-                        const int row = dg * 16 + wd * 4 + f;
+                        const int row = dg * 8 + wd * 4 + f;
                         *reinterpret_cast<uint4*>(at + row * 128 + (((tg & 7) ^ (row & 7)) << 4)) =
                             make_uint4(o[f][0], o[f][1], o[f][2], o[f][3]);
                     }
@@ -585,7 +602,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
 #pragma unroll
                     for (int i = 0; i < PIECES * D / 16; ++i) {
                         const int pc = i / (D / 16), k = i % (D / 16);
-                        mma_smem(tmem + buf * TN, tile_desc(a0 + pc * C::Q_BYTES + (k >> 2) * (PF_ROWS * 128) + (k & 3) * 32),
+                        mma_smem(tmem + (2 * s + buf) * TN,
+                                 tile_desc(a0 + pc * C::Q_BYTES + (k >> 2) * (PF_ROWS * 128) + (k & 3) * 32),
                                  tile_desc(b0 + (k >> 2) * (TN * 128) + (k & 3) * 32), mma_desc(TN), i > 0);
                     }
                 }
@@ -596,8 +614,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
 #pragma unroll
                     for (int i = 0; i < PIECES * TN / 16; ++i) {
                         const int pc = i / (TN / 16), k = i % (TN / 16);
-                        mma_tmem(tmem + C::O_COL + s * D, tmem + buf * TN + pc * (TN / 2) + k * 8,
-                                 tile_desc(b0 + (k >> 2) * (D * 128) + (k & 3) * 32), mma_desc(D), add || i > 0);
+                        mma_tmem(tmem + C::O_COL + s * D, tmem + (2 * s + buf) * TN + pc * (TN / 2) + k * 8,
+                                 tile_desc(b0 + k * 32), mma_desc(D), add || i > 0);
                     }
                 }
             };
@@ -619,43 +637,30 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 tc_after();
 #pragma unroll 1
                 for (int s = 0; s < R; ++s) {
-                    scores(s, s, 0);
-                    scores_out(&s_full[s]);
+                    scores(s, 0, 0);
+                    scores_out(&s_full[s][0]);
                 }
                 commit(&k_empty[0]);
             }
 #pragma unroll 1
             for (int j = 0; j < tiles && live; ++j) {
                 const int st = j % ST, nst = (j + 1) % ST;
-                if constexpr (R == 1) {
-                    if (j + 1 < tiles) {
-                        if (!wait(&k_full[nst], (j + 1) / ST)) break;
-                        tc_after();
-                        scores(0, (j + 1) & 1, nst);
-                        scores_out(&s_full[(j + 1) & 1]);
-                        commit(&k_empty[nst]);
-                    }
-                    if (!wait(&v_full[st], j / ST) || !wait(&p_ready[j & 1], j >> 1)) break;
-                    tc_after();
-                    values(0, j & 1, st, j > 0);
-                    commit(&pv_done);
-                    commit(&v_empty[st]);
-                } else {
-                    if (!wait(&v_full[st], j / ST)) break;
 #pragma unroll 1
-                    for (int s = 0; s < R; ++s) {
-                        if (!wait(&p_ready[s], j)) break;
+                for (int s = 0; s < R; ++s) {
+                    // the next tile's scores, into the buffer whose weights the last product has read
+                    // (matrix instructions of one thread run in order)
+                    if (j + 1 < tiles) {
+                        if (s == 0 && !wait(&k_full[nst], (j + 1) / ST)) break;
                         tc_after();
-                        values(s, s, st, j > 0);
-                        if (s == R - 1) commit(&v_empty[st]);
-                        if (j + 1 < tiles) {
-                            if (s == 0 && !wait(&k_full[nst], (j + 1) / ST)) break;
-                            tc_after();
-                            scores(s, s, nst);
-                            scores_out(&s_full[s]);
-                            if (s == R - 1) commit(&k_empty[nst]);
-                        }
+                        scores(s, (j + 1) & 1, nst);
+                        scores_out(&s_full[s][(j + 1) & 1]);
+                        if (s == R - 1) commit(&k_empty[nst]);
                     }
+                    if ((s == 0 && !wait(&v_full[st], j / ST)) || !wait(&p_ready[s][j & 1], j >> 1)) break;
+                    tc_after();
+                    values(s, j & 1, st, j > 0);
+                    commit(&pv_done[s]);
+                    if (s == R - 1) commit(&v_empty[st]);
                 }
             }
             if (live)
