@@ -18,6 +18,8 @@
 // (D <= 128, all of TMEM) share each widened tile, at D = 256 one fits.
 // The softmax reference m moves only when a score leaves it by more than 2^4; O is then
 // rescaled in TMEM by the row's own thread.  Every wait is bounded.
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace qg {
@@ -133,6 +135,11 @@ __device__ __forceinline__ float2 unpair(unsigned long long v) {
 __device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
     unsigned long long d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 __device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
@@ -387,9 +394,15 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             float m = -INFINITY;
 #pragma unroll
             for (int q = 0; q < TN / 16; ++q) {
-                float y = __uint_as_float(v[q >> 1][16 * (q & 1)]);
+                const uint32_t* x = &v[q >> 1][16 * (q & 1)];
+                float y = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+                float z = max3(__uint_as_float(x[3]), __uint_as_float(x[4]), __uint_as_float(x[5]));
 #pragma unroll
-                for (int e = 1; e < 16; ++e) y = fmaxf(y, __uint_as_float(v[q >> 1][16 * (q & 1) + e]));
+                for (int e = 6; e < 14; e += 4) {
+                    y = max3(y, __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                    z = max3(z, __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3]));
+                }
+                y = max3(y, z, fmaxf(__uint_as_float(x[14]), __uint_as_float(x[15])));
                 m = fmaxf(m, y * f[q]);
             }
             if (__any_sync(0xffffffffu, m > mo + (P_BITS + P_SLACK))) {
@@ -410,31 +423,53 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                     }
                 }
             }
-            // weights; a hidden token's is 0 whatever its block's scale holds
             const unsigned long long mo2 = pair(-mo, -mo);
+            // one piece of 16 columns; MASKED: a hidden token's weight is 0 whatever its block's scale holds
+            auto weights = [&](auto masked, int q, uint32_t* w, uint32_t* w2) {
+                unsigned long long x[8], la = 0ull, lb = 0ull;
+                const unsigned long long f2 = pair(f[q], f[q]), u2 = pair(u[q], u[q]);
+                const uint32_t* r_ = &v[q >> 1][16 * (q & 1)];
 #pragma unroll
-            for (int q = 0; q < TN / 32; ++q) {
-                uint32_t w[16], w2[16];
+                for (int e = 0; e < 8; ++e)
+                    x[e] = fma2(pair(__uint_as_float(r_[2 * e]), __uint_as_float(r_[2 * e + 1])), f2, mo2);
 #pragma unroll
-                for (int e = 0; e < 32; e += 2) {
-                    const int i = 32 * q + e;
-                    const float fi = f[i >> 4], ui = u[i >> 4];
-                    const float2 x = unpair(fma2(pair(__uint_as_float(v[q][e]), __uint_as_float(v[q][e + 1])), pair(fi, fi), mo2));
-                    const unsigned long long pp = pair(ex2(x.x), ex2(x.y));
-                    l = add2(l, pp);
-                    float2 a = unpair(mul2(pp, pair(ui, ui)));
-                    if (!plain) {
-                        const float2 z = unpair(pp);
+                for (int e = 0; e < 8; ++e) {
+                    const float2 y = unpair(x[e]);
+                    x[e] = pair(ex2(y.x), ex2(y.y));
+                }
+#pragma unroll
+                for (int e = 0; e < 8; e += 2) {
+                    la = e ? add2(la, x[e]) : x[e];
+                    lb = e ? add2(lb, x[e + 1]) : x[e + 1];
+                }
+                l = add2(l, add2(la, lb));
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float2 a = unpair(mul2(x[e], u2));
+                    if (decltype(masked)::value) {
+                        const float2 z = unpair(x[e]);
                         if (z.x == 0.0f) a.x = 0.0f;
                         if (z.y == 0.0f) a.y = 0.0f;
                     }
                     const __half2 hi2 = __floats2half2_rn(a.x, a.y);
-                    w[e / 2] = *reinterpret_cast<const uint32_t*>(&hi2);
-                    if constexpr (PIECES == 2) w2[e / 2] = half2_bits(a.x - __low2float(hi2), a.y - __high2float(hi2));
+                    w[e] = *reinterpret_cast<const uint32_t*>(&hi2);
+                    if constexpr (PIECES == 2) w2[e] = half2_bits(a.x - __low2float(hi2), a.y - __high2float(hi2));
                 }
-                tmem_store16(st + 16 * q, w);
-                if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + 16 * q, w2);
-            }
+            };
+            auto all_weights = [&](auto masked) {
+#pragma unroll
+                for (int q = 0; q < TN / 16; q += 2) {
+                    uint32_t w[16], w2[16];
+                    weights(masked, q, w, w2);
+                    weights(masked, q + 1, w + 8, w2 + 8);
+                    tmem_store16(st + 8 * q, w);
+                    if constexpr (PIECES == 2) tmem_store16(st + TN / 2 + 8 * q, w2);
+                }
+            };
+            if (plain)
+                all_weights(std::false_type{});
+            else
+                all_weights(std::true_type{});
             tmem_store_wait();
             tc_before();
             bar_arrive(&p_ready[s][buf]);
