@@ -82,6 +82,12 @@ __device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_
 __device__ __forceinline__ void tc_commit(uint64_t* b) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(b)) : "memory");
 }
+// lane 0's value in every lane: what a warp branches on and addresses matrix instructions
+// with stays in uniform registers
+template <typename T>
+__device__ __forceinline__ T uniform(T v) {
+    return __shfl_sync(0xffffffffu, v, 0);
+}
 // true in one lane of the converged warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t yes;
@@ -201,7 +207,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     unsigned char* kst = qs + R * PIECES * C::Q_BYTES;
     unsigned char* vst = kst + ST * C::K_BYTES;
 
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = uniform(tid >> 5);
     pdl_wait();
     pdl_launch_dependents();
 
@@ -225,7 +231,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     const int at0 = pos0 + (int)(row0 / p.group), at1 = pos0 + (int)((row0 + rows - 1) / p.group);
     const int lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
     const int t_begin = lo_min & ~15, t_end = at1 + 1;
-    const int tiles = t_end > t_begin ? (t_end - t_begin + TN - 1) / TN : 0;
+    const int tiles = uniform(t_end > t_begin ? (t_end - t_begin + TN - 1) / TN : 0);
     const int esize = PIECES == 2 ? 4 : 2;
 
     auto row_at = [&](const void* basep, long long stride, int r) {  // row r of this CTA in q or out
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     tc_before();
     __syncthreads();
     tc_after();
-    const uint32_t tmem = tmem_s;
+    const uint32_t tmem = uniform(tmem_s);
     const float v_ref = __uint_as_float(v_top & 0x7f800000u);  // a power of two (0: every scale is 0 or subnormal)
     const float v_inv = v_ref > 0.0f ? 1.0f / v_ref : 0.0f;
     bool live = true;
@@ -626,14 +632,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         }
     } else if (warp == 12) {
         // ================================ the matrix instructions: the warp runs as one, a lane issues
-        // (descriptors are then warp-uniform; issued from a divergent branch an instruction took
-        // over 100 cycles to set up)
+        // (with operands that are not known to be uniform across the warp each instruction took
+        // about 100 cycles to set up, whatever its size)
         {
-            const bool leader = elect_one();
-            const uint32_t q0 = smem_addr(qs), k0 = smem_addr(kst), v0 = smem_addr(vst);
+            const uint32_t q0 = uniform(smem_addr(qs)), k0 = uniform(smem_addr(kst)), v0 = uniform(smem_addr(vst));
             auto scores = [&](int s, int buf, int st) {
                 const uint32_t a0 = q0 + s * PIECES * C::Q_BYTES, b0 = k0 + st * C::K_BYTES;
-                if (leader) {
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < PIECES * D / 16; ++i) {
                         const int pc = i / (D / 16), k = i % (D / 16);
@@ -645,7 +650,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             };
             auto values = [&](int s, int buf, int st, bool add) {
                 const uint32_t b0 = v0 + st * C::K_BYTES;
-                if (leader) {
+                if (elect_one()) {
 #pragma unroll
                     for (int i = 0; i < PIECES * TN / 16; ++i) {
                         const int pc = i / (TN / 16), k = i % (TN / 16);
@@ -657,13 +662,13 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             // the products' completion, and this thread's own arrival: it has seen the tile's
             // scales (k_full), so whoever waits here sees them too
             auto scores_out = [&](uint64_t* bar) {
-                if (leader) {
+                if (elect_one()) {
                     tc_commit(bar);
                     bar_arrive(bar);
                 }
             };
             auto commit = [&](uint64_t* bar) {
-                if (leader) tc_commit(bar);
+                if (elect_one()) tc_commit(bar);
             };
             auto wait = [&](uint64_t* bar, int phase) {
                 return live = live && __all_sync(0xffffffffu, bar_wait(bar, phase & 1, &stop, p.err));
