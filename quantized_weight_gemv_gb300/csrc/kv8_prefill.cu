@@ -128,8 +128,11 @@ __device__ __forceinline__ void tmem_wait64(uint32_t (&v)[32], uint32_t (&z)[32]
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0), QG_X8(v, 8), QG_X8(v, 16), QG_X8(v, 24)::"memory");
     asm volatile("" : QG_X8(z, 0), QG_X8(z, 8), QG_X8(z, 16), QG_X8(z, 24)::"memory");
 }
-__device__ __forceinline__ void tmem_wait32(uint32_t (&v)[32]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0), QG_X8(v, 8), QG_X8(v, 16), QG_X8(v, 24)::"memory");
+__device__ __forceinline__ void tmem_request8(uint32_t at, uint32_t (&v)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];" : QG_R8(v, 0) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void tmem_wait8(uint32_t (&v)[8]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0)::"memory");
 }
 // two fp32 lanes of one register pair
 __device__ __forceinline__ unsigned long long pair(float a, float b) {
@@ -157,10 +160,6 @@ __device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigne
     unsigned long long d;
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
-}
-__device__ __forceinline__ void tmem_load32(uint32_t at, uint32_t (&v)[32]) {
-    tmem_request32(at, v);
-    tmem_wait32(v);
 }
 __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
     asm volatile(
@@ -486,17 +485,21 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             const float sum = unpair(l).x + unpair(l).y;
             const float scale = sum > 0.0f ? v_ref / sum : (sum == 0.0f ? 0.0f : sum);
             unsigned char* out = r < rows ? const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)) : nullptr;
+            // columns i D/8 + dg hold values 8 dg + i: 64 values at a time
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t v[32];
-                tmem_load32(lanes + C::O_COL + s * D + c, v);
+            for (int c = 0; c < D / 8; c += 8) {
+                uint32_t v[8][8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tmem_request8(lanes + C::O_COL + s * D + i * (D / 8) + c, v[i]);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) tmem_wait8(v[i]);
                 if (!out) continue;
 #pragma unroll
-                for (int e = 0; e < 32; e += 8) {
+                for (int e = 0; e < 8; ++e) {
                     float x[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = sum == 0.0f ? 0.0f : __uint_as_float(v[e + i]) * scale;
-                    unsigned char* at = out + (c + e) * esize;
+                    for (int i = 0; i < 8; ++i) x[i] = sum == 0.0f ? 0.0f : __uint_as_float(v[i][e]) * scale;
+                    unsigned char* at = out + 8 * (c + e) * esize;
                     if constexpr (PIECES == 2)
                         store8(reinterpret_cast<float*>(at), x);
                     else if (p.dtype == QG_DTYPE_F16)
@@ -546,8 +549,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         auto load_k = [&](int j) {
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
-                const int e = i * 128 + ct, row = (e >> 2) % TN, db = (e >> 2) / TN;
-                kr[i] = ldg_stream16(p.c.k + (slots[j & 1][row >> 4] + (row & 15)) * D + db * 64 + (e & 3) * 16);
+                const int e = i * 128 + ct, row = e / (D / 16);
+                kr[i] = ldg_stream16(p.c.k + (slots[j & 1][row >> 4] + (row & 15)) * D + e % (D / 16) * 16);
             }
         };
         auto load_v = [&](int j) {
@@ -555,7 +558,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             for (int i = 0; i < VI; ++i) {
                 const int e = i * 128 + ct;
                 if (VBLK < 128 && e >= VBLK) break;
-                const int tg = e % (TN / 8), dg = e / (TN / 8), tok = t_begin + j * TN + tg * 8;
+                const int dg = e % (D / 8), tg = e / (D / 8), tok = t_begin + j * TN + tg * 8;
                 const uint8_t* at = p.c.v + (slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 8;
                 // slots that no row sees may hold anything, an 8-bit NaN too
                 const bool edge = FMT == QG_KV8_E4M3 && (tok + 8 > t_end || tok < lo_min || ((info[j & 3].hidden >> (tg >> 1)) & 1));
@@ -581,16 +584,17 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             unsigned char* kt = kst + st * C::K_BYTES;
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
-                const int e = i * 128 + ct, row = (e >> 2) % TN, db = (e >> 2) / TN;
+                const int e = i * 128 + ct, row = e / (D / 16), db = e % (D / 16) >> 2;
                 uint4 a, z;
                 codes_to_half<FMT>(kr[i].x, a.x, a.y);
                 codes_to_half<FMT>(kr[i].y, a.z, a.w);
                 codes_to_half<FMT>(kr[i].z, z.x, z.y);
                 codes_to_half<FMT>(kr[i].w, z.z, z.w);
                 unsigned char* at = kt + db * (TN * 128) + row * 128;
-                const int c = (e & 3) * 2;
-                *reinterpret_cast<uint4*>(at + ((c ^ (row & 7)) << 4)) = a;
-                *reinterpret_cast<uint4*>(at + (((c + 1) ^ (row & 7)) << 4)) = z;
+                // lanes of an odd block store their second half first: eight lanes, eight banks of 16 bytes
+                const int c = ((e & 3) * 2) ^ (row & 7) ^ (db & 1);
+                *reinterpret_cast<uint4*>(at + (c << 4)) = db & 1 ? z : a;
+                *reinterpret_cast<uint4*>(at + ((c ^ 1) << 4)) = db & 1 ? a : z;
             }
             fence_async_smem();
             bar_arrive(&k_full[st]);
@@ -606,8 +610,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             for (int i = 0; i < VI; ++i) {
                 const int e = i * 128 + ct;
                 if (VBLK < 128 && e >= VBLK) break;
-                const int tg = e % (TN / 8), dg = e / (TN / 8);
-                unsigned char* at = vt_ + (tg >> 3) * (D * 128);
+                const int dg = e % (D / 8), tg = e / (D / 8);
+                // value 8 dg + i sits in row i D/8 + dg: eight lanes' rows then differ in the swizzle's
+                // three bits (the output's columns come back in this order too)
+                unsigned char* at = vt_;
 #pragma unroll
                 for (int wd = 0; wd < 2; ++wd) {
                     uint32_t o[4][4];  // [value][token pair]
@@ -620,7 +626,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                     }
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
-                        const int row = dg * 8 + wd * 4 + f;
+                        const int row = (wd * 4 + f) * (D / 8) + dg;
                         *reinterpret_cast<uint4*>(at + row * 128 + (((tg & 7) ^ (row & 7)) << 4)) =
                             make_uint4(o[f][0], o[f][1], o[f][2], o[f][3]);
                     }
