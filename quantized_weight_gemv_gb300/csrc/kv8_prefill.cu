@@ -59,22 +59,21 @@ __device__ __forceinline__ bool bar_try(uint64_t* b, unsigned parity) {
         : "memory");
     return ok != 0;
 }
-// false once the wait has run out here or anywhere in the CTA
-__device__ __noinline__ bool bar_wait_slow(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
+// A converged warp's wait: false once it has run out here or anywhere in the CTA.
+__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
+    if (__all_sync(0xffffffffu, bar_try(b, parity))) return true;
     const unsigned long long t0 = globaltimer_ns();
-    while (!bar_try(b, parity)) {
-        if (*stop) return false;
-        if (globaltimer_ns() - t0 > WAIT_LIMIT_NS) {
-            *stop = 1;
-            atomicOr(err, ERR_WAIT_FULL);
+    while (!__all_sync(0xffffffffu, bar_try(b, parity))) {
+        const bool late = globaltimer_ns() - t0 > WAIT_LIMIT_NS;
+        if (__any_sync(0xffffffffu, late || *stop)) {
+            if (late) {
+                *stop = 1;
+                atomicOr(err, ERR_WAIT_FULL);
+            }
             return false;
         }
     }
     return true;
-}
-__device__ __forceinline__ bool bar_wait(uint64_t* b, unsigned parity, volatile int* stop, unsigned* err) {
-    if (bar_try(b, parity)) return true;
-    return bar_wait_slow(b, parity, stop, err);
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -365,7 +364,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         unsigned long long l = 0ull;  // two sums
         for (int j = 0; j < tiles && live; ++j) {
             const int buf = j & 1, phase = (j >> 1) & 1;
-            live = __all_sync(0xffffffffu, bar_wait(&s_full[s][buf], phase, &stop, p.err));
+            live = bar_wait(&s_full[s][buf], phase, &stop, p.err);
             if (!live) break;
             tc_after();
             const uint32_t st = lanes + (2 * s + buf) * TN;
@@ -415,7 +414,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 l = mul2(l, pair(by, by));
                 mo = to;
                 if (j > 0) {  // the last product may still be running
-                    live = __all_sync(0xffffffffu, bar_wait(&pv_done[s], (j - 1) & 1, &stop, p.err));
+                    live = bar_wait(&pv_done[s], (j - 1) & 1, &stop, p.err);
                     if (!live) break;
                     tc_after();
 #pragma unroll 1
@@ -479,7 +478,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             tc_before();
             bar_arrive(&p_ready[s][buf]);
         }
-        if (live) live = __all_sync(0xffffffffu, bar_wait(&o_full[s], 0, &stop, p.err));
+        if (live) live = bar_wait(&o_full[s], 0, &stop, p.err);
         if (live) {
             tc_after();
             const float sum = unpair(l).x + unpair(l).y;
@@ -579,7 +578,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         load_v(0);
         for (int j = 0; j < tiles; ++j) {
             const int st = j % ST, phase = ((j / ST) & 1) ^ 1;
-            live = __all_sync(0xffffffffu, bar_wait(&k_empty[st], phase, &stop, p.err));
+            live = bar_wait(&k_empty[st], phase, &stop, p.err);
             if (!live) break;
             unsigned char* kt = kst + st * C::K_BYTES;
 #pragma unroll
@@ -603,7 +602,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                 load_k(j + 1);
                 request(j + 2);
             }
-            live = __all_sync(0xffffffffu, bar_wait(&v_empty[st], phase, &stop, p.err));
+            live = bar_wait(&v_empty[st], phase, &stop, p.err);
             if (!live) break;
             unsigned char* vt_ = vst + st * C::K_BYTES;
 #pragma unroll
@@ -676,41 +675,50 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             auto commit = [&](uint64_t* bar) {
                 if (elect_one()) tc_commit(bar);
             };
-            auto wait = [&](uint64_t* bar, int phase) {
-                return live = live && __all_sync(0xffffffffu, bar_wait(bar, phase & 1, &stop, p.err));
-            };
-            if (wait(&k_full[0], 0)) {
-                tc_after();
-#pragma unroll 1
-                for (int s = 0; s < R; ++s) {
-                    scores(s, 0, 0);
-                    scores_out(&s_full[s][0]);
+            auto wait = [&](uint64_t* bar, int phase) { bar_wait(bar, phase & 1, &stop, p.err); };
+            // Tile j: buffers, row tile and stage are constants of the unrolled code and nothing
+            // leaves the loop early (a wait that ran out lets the rest pass): operands that are
+            // not known to be uniform cost about 100 cycles per matrix instruction.
+            auto tile = [&](int j, auto parity) {
+                constexpr int BUF = decltype(parity)::value, NEXT = BUF ^ 1;
+                constexpr int SG = ST == 2 ? BUF : 0, SGN = ST == 2 ? NEXT : 0;
+                const bool more = j + 1 < tiles;
+                if (more) {
+                    wait(&k_full[SGN], (j + 1) / ST);
+                    tc_after();
                 }
-                commit(&k_empty[0]);
-            }
-#pragma unroll 1
-            for (int j = 0; j < tiles && live; ++j) {
-                const int st = j % ST, nst = (j + 1) % ST;
-#pragma unroll 1
+#pragma unroll
                 for (int s = 0; s < R; ++s) {
                     // the next tile's scores, into the buffer whose weights the last product has read
                     // (matrix instructions of one thread run in order)
-                    if (j + 1 < tiles) {
-                        if (s == 0 && !wait(&k_full[nst], (j + 1) / ST)) break;
-                        tc_after();
-                        scores(s, (j + 1) & 1, nst);
-                        scores_out(&s_full[s][(j + 1) & 1]);
-                        if (s == R - 1) commit(&k_empty[nst]);
+                    if (more) {
+                        scores(s, NEXT, SGN);
+                        scores_out(&s_full[s][NEXT]);
+                        if (s == R - 1) commit(&k_empty[SGN]);
                     }
-                    if ((s == 0 && !wait(&v_full[st], j / ST)) || !wait(&p_ready[s][j & 1], j >> 1)) break;
+                    if (s == 0) wait(&v_full[SG], j / ST);
+                    wait(&p_ready[s][BUF], j >> 1);
                     tc_after();
-                    values(s, j & 1, st, j > 0);
+                    values(s, BUF, SG, j > 0);
                     commit(&pv_done[s]);
-                    if (s == R - 1) commit(&v_empty[st]);
+                    if (s == R - 1) commit(&v_empty[SG]);
                 }
+            };
+            wait(&k_full[0], 0);
+            tc_after();
+#pragma unroll
+            for (int s = 0; s < R; ++s) {
+                scores(s, 0, 0);
+                scores_out(&s_full[s][0]);
             }
-            if (live)
-                for (int s = 0; s < R; ++s) commit(&o_full[s]);
+            commit(&k_empty[0]);
+#pragma unroll 1
+            for (int j = 0; j < tiles; j += 2) {
+                tile(j, std::integral_constant<int, 0>{});
+                if (j + 1 < tiles) tile(j + 1, std::integral_constant<int, 1>{});
+            }
+#pragma unroll
+            for (int s = 0; s < R; ++s) commit(&o_full[s]);
             // nothing may be in flight when TMEM is given back
             commit(&drained);
             const unsigned long long t0 = globaltimer_ns();
