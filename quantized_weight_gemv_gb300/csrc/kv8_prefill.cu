@@ -10,9 +10,9 @@
 // two among the CTA's blocks) onto P.  Queries are brought to [-1, 1] by a power of two per
 // row; fp32 queries and weights enter as two binary16 pieces, two products each.
 //
-// Roles (13 warps): one warpgroup per row tile does the softmax, a thread per row; one
-// warpgroup widens the next tile's codes from registers into the 128-byte-swizzled K-major
-// tiles that the matrix instructions read (V transposed on the way: pairs of tokens are
+// Roles (16 warps): one warpgroup per row tile does the softmax, a thread per row; four warps
+// widen the next tile's K codes from registers into the 128-byte-swizzled K-major tiles that
+// the matrix instructions read, three V's (transposed on the way: pairs of tokens are
 // interleaved by byte permutes); one warp issues.  S is double-buffered, so the scores of
 // the next tile are ready when a row tile's softmax has finished this one; R = 2 row tiles
 // (D <= 128, all of TMEM) share each widened tile, at D = 256 one fits.
@@ -25,7 +25,8 @@
 namespace qg {
 namespace kv8 {
 
-constexpr int PF_THREADS = 416;
+constexpr int PF_THREADS = 512;  // 8 warps softmax, 4 widen K, 1 issues, 3 widen V
+constexpr int V_THREADS = 96;
 constexpr int PF_ROWS = 128;  // rows of one matrix instruction
 
 template <int D, int PIECES>
@@ -176,7 +177,8 @@ __device__ __forceinline__ void tmem_store16(uint32_t at, const uint32_t (&v)[16
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// what the softmax needs of one token tile, in a ring of four
+// what the softmax needs of one token tile, in a ring of eight: K's warps publish a tile at
+// most five tiles ahead of the softmax that still reads its own
 template <int TN>
 struct TileInfo {
     float ks[TN / 16];  // K's scale of each 16 tokens
@@ -184,8 +186,11 @@ struct TileInfo {
     int hidden;         // bit i: these 16 tokens could not be read
 };
 
-// the widening warpgroup's own barrier
-__device__ __forceinline__ void convert_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// the widening warps' own barriers
+template <int ID, int THREADS>
+__device__ __forceinline__ void group_sync() {
+    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
+}
 
 template <int D, int FMT, int PIECES>
 __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams p) {
@@ -194,8 +199,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], o_full[2], pv_done[2], drained;
     __shared__ uint64_t s_full[2][2], p_ready[2][2];  // [row tile][S buffer]
-    __shared__ TileInfo<TN> info[4];
-    __shared__ long long slots[2][TN / 16];  // the token slots of a tile's blocks of 16 (widening warpgroup)
+    __shared__ TileInfo<TN> info[8];
+    // the token slots of a tile's blocks of 16, for K's and V's warps
+    __shared__ long long k_slots[2][TN / 16], v_slots[2][TN / 16];
+    __shared__ int v_hidden[2];
     __shared__ float row_factor[RR];
     __shared__ unsigned v_top;  // the largest value scale, as bits
     __shared__ int stop;
@@ -251,7 +258,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             bar_init(&k_full[i], 128);
-            bar_init(&v_full[i], 128);
+            bar_init(&v_full[i], V_THREADS);
             bar_init(&k_empty[i], 1);
             bar_init(&v_empty[i], 1);
             for (int k = 0; k < 2; ++k) {
@@ -273,8 +280,8 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     __syncthreads();  // v_top is zero
     const int32_t* table = p.c.table + (long long)b * p.c.max_pages;
     const int pmask = (1 << p.c.page_log2) - 1;
-    auto slot_of = [&](int tok, bool& ok) {  // token slot of `tok`, page 0 where it cannot be read
-        const int page = tok < t_end ? table[tok >> p.c.page_log2] : -1;
+    auto page_of = [&](int tok) { return tok < t_end ? table[tok >> p.c.page_log2] : -1; };
+    auto slot_in = [&](int page, int tok, bool& ok) {  // token slot of `tok`, page 0 where it cannot be read
         ok = (unsigned)page < (unsigned)p.c.n_pages;
         return slot_base(p.c, ok ? page : 0, h) + (tok & pmask);
     };
@@ -282,7 +289,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         unsigned top = 0u;
         for (int tok = t_begin + tid * 16; tok < t_end; tok += PF_THREADS * 16) {
             bool ok;
-            const long long s = slot_of(tok, ok);
+            const long long s = slot_in(page_of(tok), tok, ok);
             const float v = p.c.vs[s >> p.c.block_log2];
             if (ok && v < INFINITY && v > 0.0f) top = max(top, __float_as_uint(v));
             if (!ok) atomicOr(p.err, ERR_KV_RANGE);
@@ -371,7 +378,7 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             uint32_t v[2][32];
             tmem_request32(st, v[0]);
             tmem_request32(st + 32, v[1]);
-            const TileInfo<TN>& ti = info[j & 3];
+            const TileInfo<TN>& ti = info[j & 7];
             const int tok = t_begin + j * TN;
             const int hidden = ti.hidden;
             const bool plain = !cap && !hidden && tok + TN - 1 <= hi_min && tok >= lo_max;
@@ -515,67 +522,51 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             tc_before();
         }
     } else if (warp >= 8 && warp < 12) {
-        // ================================ widening: codes to binary16 tiles
+        // ================================ K's codes to binary16 tiles
         const int ct = tid - 256;
-        constexpr int KI = TN * D / 16 / 128;         // 16-byte pieces of K per thread
-        constexpr int VBLK = TN / 8 * (D / 8);        // V blocks of 8 tokens x 8 values
-        constexpr int VI = (VBLK + 127) / 128;
+        constexpr int KI = TN * D / 16 / 128;  // 16-byte pieces per thread
         uint4 kr[KI];
-        uint2 vr[VI][8];
-        // A tile's slots, and what the softmax needs of it, are requested a tile ahead (by the
-        // first TN / 16 threads) and published at a barrier.
+        // What a tile's loads and softmax need is looked up ahead, by the first TN / 16 threads:
+        // its page ids two tiles before, its scales one, and published at a barrier.
+        int page = -1;
         long long next_slot = 0;
         float next_ks = 0.0f, next_u = 0.0f;
         bool next_ok = false;
-        auto request = [&](int j) {
+        auto request_page = [&](int j) {
+            if (ct < TN / 16) page = page_of(t_begin + j * TN + ct * 16);
+        };
+        auto request_scales = [&](int j) {
             if (ct < TN / 16) {
-                next_slot = slot_of(t_begin + j * TN + ct * 16, next_ok);
+                next_slot = slot_in(page, t_begin + j * TN + ct * 16, next_ok);
                 next_ks = p.c.ks[next_slot >> p.c.block_log2];
                 next_u = p.c.vs[next_slot >> p.c.block_log2];
             }
         };
         auto publish = [&](int j) {
             if (ct < TN / 16) {
-                TileInfo<TN>& ti = info[j & 3];
-                slots[j & 1][ct] = next_slot;
+                TileInfo<TN>& ti = info[j & 7];
+                k_slots[j & 1][ct] = next_slot;
                 ti.ks[ct] = next_ok ? next_ks : 0.0f;
                 ti.u[ct] = next_ok ? next_u * v_inv : 0.0f;
                 const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, t_begin + j * TN + ct * 16 < t_end && !next_ok);
                 if (ct == 0) ti.hidden = (int)hid;
             }
-            convert_sync();
+            group_sync<1, 128>();
         };
         auto load_k = [&](int j) {
 #pragma unroll
             for (int i = 0; i < KI; ++i) {
                 const int e = i * 128 + ct, row = e / (D / 16);
-                kr[i] = ldg_stream16(p.c.k + (slots[j & 1][row >> 4] + (row & 15)) * D + e % (D / 16) * 16);
+                kr[i] = ldg_stream16(p.c.k + (k_slots[j & 1][row >> 4] + (row & 15)) * D + e % (D / 16) * 16);
             }
         };
-        auto load_v = [&](int j) {
-#pragma unroll
-            for (int i = 0; i < VI; ++i) {
-                const int e = i * 128 + ct;
-                if (VBLK < 128 && e >= VBLK) break;
-                const int dg = e % (D / 8), tg = e / (D / 8), tok = t_begin + j * TN + tg * 8;
-                const uint8_t* at = p.c.v + (slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 8;
-                // slots that no row sees may hold anything, an 8-bit NaN too
-                const bool edge = FMT == QG_KV8_E4M3 && (tok + 8 > t_end || tok < lo_min || ((info[j & 3].hidden >> (tg >> 1)) & 1));
-#pragma unroll
-                for (int k = 0; k < 8; ++k) vr[i][k] = ldg_stream8(at + k * D);
-                if (edge) {
-                    const bool all = (info[j & 3].hidden >> (tg >> 1)) & 1;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (all || tok + k >= t_end || tok + k < lo_min) vr[i][k] = make_uint2(0u, 0u);
-                }
-            }
-        };
-        request(0);
+        request_page(0);
+        request_scales(0);
+        request_page(1);
         publish(0);
-        request(1);
         load_k(0);
-        load_v(0);
+        request_scales(1);
+        request_page(2);
         for (int j = 0; j < tiles; ++j) {
             const int st = j % ST, phase = ((j / ST) & 1) ^ 1;
             live = bar_wait(&k_empty[st], phase, &stop, p.err);
@@ -600,40 +591,90 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             if (j + 1 < tiles) {
                 publish(j + 1);
                 load_k(j + 1);
-                request(j + 2);
+                request_scales(j + 2);
+                request_page(j + 3);
             }
-            live = bar_wait(&v_empty[st], phase, &stop, p.err);
-            if (!live) break;
-            unsigned char* vt_ = vst + st * C::K_BYTES;
+        }
+    } else if (warp > 12) {
+        // ================================ V's codes to binary16 tiles, transposed
+        const int ct = tid - 416;
+        constexpr int BLOCKS = TN / 8 * (D / 8);  // of 8 tokens x 8 values
+        constexpr int VI = (BLOCKS + V_THREADS - 1) / V_THREADS;
+        uint2 vr[VI][8];
+        int page = -1;
+        auto request_page = [&](int j) {
+            if (ct < TN / 16) page = page_of(t_begin + j * TN + ct * 16);
+        };
+        auto publish = [&](int j) {
+            if (ct < TN / 16) {
+                bool ok;
+                v_slots[j & 1][ct] = slot_in(page, t_begin + j * TN + ct * 16, ok);
+                const unsigned hid = __ballot_sync((1u << (TN / 16)) - 1u, !ok);
+                if (ct == 0) v_hidden[j & 1] = (int)hid;
+            }
+            group_sync<2, V_THREADS>();
+        };
+        auto load_v = [&](int j) {
 #pragma unroll
             for (int i = 0; i < VI; ++i) {
-                const int e = i * 128 + ct;
-                if (VBLK < 128 && e >= VBLK) break;
+                const int e = i * V_THREADS + ct;
+                if (e >= BLOCKS) break;
+                const int dg = e % (D / 8), tg = e / (D / 8), tok = t_begin + j * TN + tg * 8;
+                const uint8_t* at = p.c.v + (v_slots[j & 1][tg >> 1] + (tg & 1) * 8) * D + dg * 8;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) vr[i][k] = ldg_stream8(at + k * D);
+                // slots that no row sees may hold anything, an 8-bit NaN too
+                if constexpr (FMT == QG_KV8_E4M3) {
+                    const bool all = (v_hidden[j & 1] >> (tg >> 1)) & 1;
+                    if (all || tok + 8 > t_end || tok < lo_min) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (all || tok + k >= t_end || tok + k < lo_min) vr[i][k] = make_uint2(0u, 0u);
+                    }
+                }
+            }
+        };
+        request_page(0);
+        publish(0);
+        request_page(1);
+        load_v(0);
+        for (int j = 0; j < tiles; ++j) {
+            const int st = j % ST, phase = ((j / ST) & 1) ^ 1;
+            live = bar_wait(&v_empty[st], phase, &stop, p.err);
+            if (!live) break;
+            unsigned char* at = vst + st * C::K_BYTES;
+#pragma unroll
+            for (int i = 0; i < VI; ++i) {
+                const int e = i * V_THREADS + ct;
+                if (e >= BLOCKS) break;
                 const int dg = e % (D / 8), tg = e / (D / 8);
                 // value 8 dg + i sits in row i D/8 + dg: eight lanes' rows then differ in the swizzle's
                 // three bits (the output's columns come back in this order too)
-                unsigned char* at = vt_;
 #pragma unroll
                 for (int wd = 0; wd < 2; ++wd) {
                     uint32_t o[4][4];  // [value][token pair]
 #pragma unroll
                     for (int tp = 0; tp < 4; ++tp) {
-                        const uint32_t a = reinterpret_cast<const uint32_t*>(&vr[i][2 * tp])[wd];
-                        const uint32_t z = reinterpret_cast<const uint32_t*>(&vr[i][2 * tp + 1])[wd];
+                        const uint32_t a = wd ? vr[i][2 * tp].y : vr[i][2 * tp].x;
+                        const uint32_t z = wd ? vr[i][2 * tp + 1].y : vr[i][2 * tp + 1].x;
                         codes_to_half<FMT>(__byte_perm(a, z, 0x5140), o[0][tp], o[1][tp]);
                         codes_to_half<FMT>(__byte_perm(a, z, 0x7362), o[2][tp], o[3][tp]);
                     }
 #pragma unroll
                     for (int f = 0; f < 4; ++f) {
                         const int row = (wd * 4 + f) * (D / 8) + dg;
-                        *reinterpret_cast<uint4*>(at + row * 128 + (((tg & 7) ^ (row & 7)) << 4)) =
+                        *reinterpret_cast<uint4*>(at + row * 128 + ((tg ^ (row & 7)) << 4)) =
                             make_uint4(o[f][0], o[f][1], o[f][2], o[f][3]);
                     }
                 }
             }
             fence_async_smem();
             bar_arrive(&v_full[st]);
-            if (j + 1 < tiles) load_v(j + 1);
+            if (j + 1 < tiles) {
+                publish(j + 1);
+                load_v(j + 1);
+                request_page(j + 2);
+            }
         }
     } else if (warp == 12) {
         // ================================ the matrix instructions: the warp runs as one, a lane issues
