@@ -723,27 +723,27 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
             auto tile = [&](int j, auto parity) {
                 constexpr int BUF = decltype(parity)::value, NEXT = BUF ^ 1;
                 constexpr int SG = ST == 2 ? BUF : 0, SGN = ST == 2 ? NEXT : 0;
-                const bool more = j + 1 < tiles;
-                if (more) {
+                // the next tile's scores, into the buffers whose weights the last products have read
+                // (matrix instructions of one thread run in order)
+                if (j + 1 < tiles) {
                     wait(&k_full[SGN], (j + 1) / ST);
                     tc_after();
-                }
 #pragma unroll
-                for (int s = 0; s < R; ++s) {
-                    // the next tile's scores, into the buffer whose weights the last product has read
-                    // (matrix instructions of one thread run in order)
-                    if (more) {
+                    for (int s = 0; s < R; ++s) {
                         scores(s, NEXT, SGN);
                         scores_out(&s_full[s][NEXT]);
-                        if (s == R - 1) commit(&k_empty[SGN]);
                     }
-                    if (s == 0) wait(&v_full[SG], j / ST);
+                    commit(&k_empty[SGN]);
+                }
+                wait(&v_full[SG], j / ST);
+#pragma unroll
+                for (int s = 0; s < R; ++s) {
                     wait(&p_ready[s][BUF], j >> 1);
                     tc_after();
                     values(s, BUF, SG, j > 0);
                     commit(&pv_done[s]);
-                    if (s == R - 1) commit(&v_empty[SG]);
                 }
+                commit(&v_empty[SG]);
             };
             wait(&k_full[0], 0);
             tc_after();
