@@ -133,8 +133,8 @@ struct AttnParams {
     long long q_stride, out_stride;
     int tokens, hq, group, dtype, window;
     float scale, softcap;
-    // the split kernel's workspace: arrival counters (zero between calls), and per CTA two
-    // partials: (reference, sum) of each row, and the rows' weighted values
+    // the workspace: arrival counters (zero between calls), and partials: (reference, sum) of
+    // each row, and the rows' weighted values
     unsigned* counter;
     float* part_ml;
     float* part_o;
@@ -192,7 +192,8 @@ __device__ __forceinline__ Sequence sequence(const AttnParams& p, int b) {
 }
 
 // many query rows per kv head (kv8_prefill.cu)
-int launch_prefill(const AttnParams& p, int format, int d, const LaunchCtx& lc);
+size_t prefill_ws_bytes(int d);
+int launch_prefill(const AttnParams& p, int format, int d, unsigned char* ws, const LaunchCtx& lc);
 
 }  // namespace kv8
 }  // namespace qg

@@ -24,7 +24,10 @@ namespace kv8 {
 
 constexpr int W = 8;            // warps per CTA
 constexpr int SUB = 16;         // cache tokens per warp step
-constexpr int PREFILL_ROWS = 64;  // query rows per sequence and kv head from which launch_prefill takes the call
+// Query rows per sequence and kv head from which launch_prefill takes the call.  Measured (us, this
+// kernel / that one): 32 rows of head_dim 128, 32 sequences x 1024: 69 / 93; 64 rows of them 120 / 94;
+// 64 rows over 8192, one sequence: 35 / 39; 128 rows 46 / 41; 512 rows 130 / 63.
+constexpr int PREFILL_ROWS = 64;
 constexpr int MAX_CTAS = 320;   // CTAs that share out one call (workspace slots)
 
 // ---------------------------------------------------------------- device helpers
@@ -615,7 +618,7 @@ static int launch_d(AttnParams& p, int d, unsigned char* ws, const LaunchCtx& lc
 
 size_t kv8_ws_bytes(int d) {
     using namespace kv8;
-    return QG_KV8_CTL_BYTES + (size_t)2 * MAX_CTAS * 16 * (d + 2) * 4;
+    return max(QG_KV8_CTL_BYTES + (size_t)2 * MAX_CTAS * 16 * (d + 2) * 4, prefill_ws_bytes(d));
 }
 
 int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, unsigned char* ws, const LaunchCtx& lc) {
@@ -627,7 +630,7 @@ int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, 
     p.tokens = a.tokens, p.hq = a.n_q_heads, p.group = a.n_q_heads / c.n_kv_heads, p.dtype = a.dtype;
     p.window = a.window, p.scale = a.scale, p.softcap = a.softcap;
     p.err = lc.err;
-    if ((long long)p.tokens * p.group / c.batch >= PREFILL_ROWS) return launch_prefill(p, c.format, c.head_dim, lc);
+    if ((long long)p.tokens * p.group / c.batch >= PREFILL_ROWS) return launch_prefill(p, c.format, c.head_dim, ws, lc);
     const bool f32 = a.dtype == QG_DTYPE_F32;
     if (c.format == QG_KV8_INT8)
         return f32 ? launch_d<QG_KV8_INT8, 2>(p, c.head_dim, ws, lc) : launch_d<QG_KV8_INT8, 1>(p, c.head_dim, ws, lc);

@@ -28,11 +28,13 @@ namespace kv8 {
 constexpr int PF_THREADS = 512;  // 8 warps softmax, 4 widen K, 1 issues, 3 widen V
 constexpr int V_THREADS = 96;
 constexpr int PF_ROWS = 128;  // rows of one matrix instruction
+constexpr int TN_TOKENS = 64; // cache tokens per tile
+constexpr int PF_SLOTS = 152; // CTAs of a call whose token tiles are split (workspace slots)
 
 template <int D, int PIECES>
 struct Prefill {
     static constexpr int R = D == 256 ? 1 : 2;            // row tiles per CTA
-    static constexpr int TN = 64;                         // cache tokens per tile
+    static constexpr int TN = TN_TOKENS;                  // cache tokens per tile
     static constexpr int ST = PIECES == 2 && D == 256 ? 1 : 2;  // K and V buffers
     static constexpr int Q_BYTES = PF_ROWS * D * 2;       // one piece of one row tile
     static constexpr int K_BYTES = TN * D * 2;
@@ -192,6 +194,39 @@ __device__ __forceinline__ void group_sync() {
     asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(THREADS) : "memory");
 }
 
+// One CTA's rows.  Sequence b owns the virtual tiles from floor(first row / RR) + b on.
+template <int RR>
+struct RowTile {
+    Sequence sq;
+    int b;
+    long long row0;  // first row (token x grouped head) within the sequence
+    int rows;        // <= 0: none
+    int pos0;        // position of the sequence's first token of the call
+    int lo_min, t_begin, t_end;  // tokens that some row sees: lo_min .. t_end - 1; t_begin: lo_min on a block of 16
+    int tiles;
+
+    __device__ __forceinline__ RowTile(const AttnParams& p, int vt) {
+        auto tile_of = [&](int i) { return (int)((long long)(p.cu ? p.cu[i] : i) * p.group / RR) + i; };
+        b = 0;
+        for (int hi = p.c.batch; hi - b > 1;) {
+            const int mid = (b + hi) >> 1;
+            if (tile_of(mid) <= vt)
+                b = mid;
+            else
+                hi = mid;
+        }
+        sq = sequence(p, b);
+        row0 = (long long)(vt - tile_of(b)) * RR;
+        rows = row0 < 0 ? 0 : (int)max(0ll, min((long long)RR, (long long)sq.n * p.group - row0));
+        pos0 = sq.len - sq.n;
+        const int at0 = pos0 + (int)(row0 / p.group), at1 = pos0 + (int)((row0 + rows - 1) / p.group);
+        lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
+        t_begin = lo_min & ~15;
+        t_end = at1 + 1;
+        tiles = t_end > t_begin ? (t_end - t_begin + TN_TOKENS - 1) / TN_TOKENS : 0;
+    }
+};
+
 template <int D, int FMT, int PIECES>
 __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams p) {
     using C = Prefill<D, PIECES>;
@@ -216,27 +251,18 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     pdl_wait();
     pdl_launch_dependents();
 
-    // the sequence and row tile: sequence b owns the virtual tiles from floor(first row / RR) + b
-    // on; the last ones come first, a causal mask makes them the longest
-    const int vt = (int)(gridDim.x - 1 - blockIdx.x), h = blockIdx.y;
-    auto tile_of = [&](int b) { return (int)((long long)(p.cu ? p.cu[b] : b) * p.group / RR) + b; };
-    int b = 0;
-    for (int hi = p.c.batch; hi - b > 1;) {
-        const int mid = (b + hi) >> 1;
-        if (tile_of(mid) <= vt)
-            b = mid;
-        else
-            hi = mid;
-    }
-    const Sequence sq = sequence(p, b);
-    const long long row0 = (long long)(vt - tile_of(b)) * RR;
-    if (row0 < 0 || row0 >= (long long)sq.n * p.group) return;
-    const int rows = (int)min((long long)RR, (long long)sq.n * p.group - row0);
-    const int pos0 = sq.len - sq.n;  // position of the sequence's first token of the call
-    const int at0 = pos0 + (int)(row0 / p.group), at1 = pos0 + (int)((row0 + rows - 1) / p.group);
-    const int lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
-    const int t_begin = lo_min & ~15, t_end = at1 + 1;
-    const int tiles = uniform(t_end > t_begin ? (t_end - t_begin + TN - 1) / TN : 0);
+    // the last row tiles come first: a causal mask makes them the longest
+    const int vt = (int)(gridDim.x - 1 - blockIdx.x), h = blockIdx.y, splits = gridDim.z;
+    const RowTile<RR> rt(p, vt);
+    if (rt.rows <= 0) return;
+    const Sequence sq = rt.sq;
+    const int b = rt.b, rows = rt.rows, pos0 = rt.pos0, lo_min = rt.lo_min, t_end = rt.t_end;
+    const long long row0 = rt.row0;
+    // this CTA's share of the token tiles
+    const int share = (rt.tiles + splits - 1) / splits;
+    const int t_begin = rt.t_begin + (int)blockIdx.z * share * TN;
+    const int tiles = uniform(min(share, rt.tiles - (int)blockIdx.z * share));
+    const long long slot = ((long long)vt * p.c.hkv + h) * splits + blockIdx.z;
     const int esize = PIECES == 2 ? 4 : 2;
 
     auto row_at = [&](const void* basep, long long stride, int r) {  // row r of this CTA in q or out
@@ -244,7 +270,12 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         return (const unsigned char*)basep +
                ((sq.t0 + rr / p.group) * stride + (long long)(h * p.group + rr % p.group) * D) * esize;
     };
-    if (tiles == 0) {  // no row sees anything
+    if (rt.tiles > 0 && tiles <= 0) {  // nothing left for this share
+        for (int r = tid; r < rows; r += PF_THREADS)
+            reinterpret_cast<float2*>(p.part_ml)[slot * RR + r] = make_float2(-1e30f, 0.0f);
+        return;
+    }
+    if (tiles <= 0) {  // no row sees anything
         for (int i = tid; i < rows * (D * esize / 16); i += PF_THREADS) {
             const int r = i / (D * esize / 16), c = i % (D * esize / 16);
             reinterpret_cast<uint4*>(const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)))[c] = make_uint4(0, 0, 0, 0);
@@ -489,7 +520,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         if (live) {
             tc_after();
             const float sum = unpair(l).x + unpair(l).y;
-            const float scale = sum > 0.0f ? v_ref / sum : (sum == 0.0f ? 0.0f : sum);
+            // a share's values stay unnormalised
+            const float scale = splits > 1 ? v_ref : sum > 0.0f ? v_ref / sum : (sum == 0.0f ? 0.0f : sum);
+            float* part = p.part_o + (slot * RR + r) * D;
             unsigned char* out = r < rows ? const_cast<unsigned char*>(row_at(p.out, p.out_stride, r)) : nullptr;
             // columns i D/8 + dg hold values 8 dg + i: 64 values at a time
 #pragma unroll 1
@@ -506,7 +539,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[i] = sum == 0.0f ? 0.0f : __uint_as_float(v[i][e]) * scale;
                     unsigned char* at = out + 8 * (c + e) * esize;
-                    if constexpr (PIECES == 2)
+                    if (splits > 1)
+                        store8(part + 8 * (c + e), x);
+                    else if constexpr (PIECES == 2)
                         store8(reinterpret_cast<float*>(at), x);
                     else if (p.dtype == QG_DTYPE_F16)
                         store8(reinterpret_cast<__half*>(at), x);
@@ -514,7 +549,9 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
                         store8(reinterpret_cast<__nv_bfloat16*>(at), x);
                 }
             }
-            if (p.lse && out) {
+            if (splits > 1) {
+                if (out) reinterpret_cast<float2*>(p.part_ml)[slot * RR + r] = make_float2(mo, sum);
+            } else if (p.lse && out) {
                 const int rr = (int)row0 + r;
                 p.lse[(long long)(sq.t0 + rr / p.group) * p.hq + h * p.group + rr % p.group] =
                     sum == 0.0f ? -INFINITY : (mo + log2f(sum)) * 0.693147180559945f;
@@ -775,33 +812,83 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
     }
 }
 
+// The shares of split row tiles added up, a warp per row.
+template <int D, int RR, typename T>
+__global__ void merge_kernel(const AttnParams p, int splits) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int vt = blockIdx.x, h = blockIdx.y, lane = threadIdx.x & 31, r = blockIdx.z * 8 + (threadIdx.x >> 5);
+    const RowTile<RR> rt(p, vt);
+    if (rt.tiles == 0 || r >= rt.rows) return;
+    const long long slot = ((long long)vt * p.c.hkv + h) * splits;
+    const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + slot * RR + r;
+    // lane i: share i's (reference, sum)
+    const float2 mine = lane < splits ? ml[(long long)lane * RR] : make_float2(-1e30f, 0.0f);
+    float m = mine.x;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float f = mine.y == 0.0f ? 0.0f : ex2(mine.x - m), sum = warp_sum(mine.y * f);
+    constexpr int PER = D / 32;
+    float acc[PER] = {};
+    const float* part = p.part_o + (slot * RR + r) * D + lane * PER;
+#pragma unroll 4
+    for (int i = 0; i < splits; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        if (fi == 0.0f) continue;  // an empty share left no values
+        float x[PER];
+        load_values(part + (long long)i * RR * D, x);
+#pragma unroll
+        for (int e = 0; e < PER; ++e) acc[e] = fmaf(x[e], fi, acc[e]);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    const int rr = (int)rt.row0 + r;
+    const long long t = rt.sq.t0 + rr / p.group, hh = h * p.group + rr % p.group;
+    T* out = reinterpret_cast<T*>(p.out) + t * p.out_stride + hh * D + lane * PER;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) from_float(acc[e] * inv, out[e]);
+    if (p.lse && lane == 0) p.lse[t * p.hq + hh] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+}
+
 template <int D, int FMT, int PIECES>
-static int launch_shape(const AttnParams& p, const LaunchCtx& lc) {
+static int launch_shape(AttnParams p, unsigned char* ws, const LaunchCtx& lc) {
     using C = Prefill<D, PIECES>;
+    constexpr int RR = C::R * PF_ROWS;
     const void* kernel = reinterpret_cast<const void*>(prefill_kernel<D, FMT, PIECES>);
-    const int rc = ensure_smem_attr(kernel, C::smem, lc);
+    int rc = ensure_smem_attr(kernel, C::smem, lc);
     if (rc != QG_OK) return rc;
-    const long long tiles = (long long)p.tokens * p.group / (C::R * PF_ROWS) + p.c.batch;
+    const long long tiles = (long long)p.tokens * p.group / RR + p.c.batch;
     if (tiles > 0x7fffffffll || p.c.hkv > 65535) return QG_ERR_UNSUPPORTED;
-    return launch_kernel(prefill_kernel<D, FMT, PIECES>, dim3((unsigned)tiles, (unsigned)p.c.hkv), dim3(PF_THREADS), C::smem, lc, p);
+    // too few row tiles for the SMs: each one's token tiles are shared out
+    const long long splits = min(32ll, max(1ll, (long long)min(PF_SLOTS, lc.sm_count) / (tiles * p.c.hkv)));
+    p.part_ml = reinterpret_cast<float*>(ws + QG_KV8_CTL_BYTES);
+    p.part_o = p.part_ml + (size_t)PF_SLOTS * RR * 2;
+    rc = launch_kernel(prefill_kernel<D, FMT, PIECES>, dim3((unsigned)tiles, (unsigned)p.c.hkv, (unsigned)splits),
+                       dim3(PF_THREADS), C::smem, lc, p);
+    if (rc != QG_OK || splits == 1) return rc;
+    const dim3 grid((unsigned)tiles, (unsigned)p.c.hkv, RR / 8);
+    if (PIECES == 2) return launch_kernel(merge_kernel<D, RR, float>, grid, dim3(256), 0, lc, p, (int)splits);
+    return p.dtype == QG_DTYPE_F16 ? launch_kernel(merge_kernel<D, RR, __half>, grid, dim3(256), 0, lc, p, (int)splits)
+                                   : launch_kernel(merge_kernel<D, RR, __nv_bfloat16>, grid, dim3(256), 0, lc, p, (int)splits);
 }
 
 template <int FMT, int PIECES>
-static int launch_d(const AttnParams& p, int d, const LaunchCtx& lc) {
+static int launch_d(const AttnParams& p, int d, unsigned char* ws, const LaunchCtx& lc) {
     switch (d) {
         case 64:
-            return launch_shape<64, FMT, PIECES>(p, lc);
+            return launch_shape<64, FMT, PIECES>(p, ws, lc);
         case 128:
-            return launch_shape<128, FMT, PIECES>(p, lc);
+            return launch_shape<128, FMT, PIECES>(p, ws, lc);
         default:
-            return launch_shape<256, FMT, PIECES>(p, lc);
+            return launch_shape<256, FMT, PIECES>(p, ws, lc);
     }
 }
 
-int launch_prefill(const AttnParams& p, int format, int d, const LaunchCtx& lc) {
+size_t prefill_ws_bytes(int d) { return QG_KV8_CTL_BYTES + (size_t)PF_SLOTS * (d == 256 ? 128 : 256) * (d + 2) * 4; }
+
+int launch_prefill(const AttnParams& p, int format, int d, unsigned char* ws, const LaunchCtx& lc) {
     const bool f32 = p.dtype == QG_DTYPE_F32;
-    if (format == QG_KV8_INT8) return f32 ? launch_d<QG_KV8_INT8, 2>(p, d, lc) : launch_d<QG_KV8_INT8, 1>(p, d, lc);
-    return f32 ? launch_d<QG_KV8_E4M3, 2>(p, d, lc) : launch_d<QG_KV8_E4M3, 1>(p, d, lc);
+    if (format == QG_KV8_INT8) return f32 ? launch_d<QG_KV8_INT8, 2>(p, d, ws, lc) : launch_d<QG_KV8_INT8, 1>(p, d, ws, lc);
+    return f32 ? launch_d<QG_KV8_E4M3, 2>(p, d, ws, lc) : launch_d<QG_KV8_E4M3, 1>(p, d, ws, lc);
 }
 
 }  // namespace kv8
