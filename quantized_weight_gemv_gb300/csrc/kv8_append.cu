@@ -2,7 +2,7 @@
 // rotated queries, in one launch.
 //
 // One CTA per (block of scale_block tokens, kv head, k or v) that the call touches: it
-// holds the block's new values in registers (at most 32 a thread), reduces their largest
+// holds the block's new values in registers (16 a thread), reduces their largest
 // magnitude, and writes the codes against the block's scale - one read of the inputs and
 // one write of the codes, nothing kept between.  A block that already holds tokens is
 // rewritten only when its scale grows, and only that block's bytes (scale_block x
@@ -70,6 +70,64 @@ __device__ __forceinline__ uint32_t to_code(float x, float s, float inv) {
     }
 }
 
+// The codes of a slot's eight values, four to a word: Q(fl(x / s)).  The quotient is taken as
+// t = x * fl(1/s), within 2^-22 of fl(x / s) in relative terms, and decides unless it lies
+// within that of a rounding boundary; then, and for NaN, infinities and scales near the
+// subnormal range, the exact division does.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+template <int FMT>
+__device__ __forceinline__ void to_codes(const float (&x)[8], float s, float inv, uint32_t (&w)[2]) {
+    bool exact = s < 1e-30f;  // also 0
+    if constexpr (FMT == QG_KV8_INT8) {
+        constexpr float MAGIC = 12582912.0f;  // 1.5 * 2^23: the sum's low byte is the rounded code
+        float r[8], far = 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float t = x[e] * inv;
+            r[e] = __fadd_rn(t, MAGIC);
+            far = max_nan(far, fabsf(t - __fsub_rn(r[e], MAGIC)));
+        }
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            const uint32_t a = __byte_perm(__float_as_uint(r[4 * f]), __float_as_uint(r[4 * f + 1]), 0x0040);
+            const uint32_t b = __byte_perm(__float_as_uint(r[4 * f + 2]), __float_as_uint(r[4 * f + 3]), 0x0040);
+            w[f] = __byte_perm(a, b, 0x5410);
+        }
+        exact |= !(far < 0.5f - 1.0f / 4096.0f);
+    } else {
+        float big = 0.0f;
+        bool same = true;
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int e = 2; e >= 0; e -= 2) {
+                const float t = x[4 * f + e] * inv, u = x[4 * f + e + 1] * inv;
+                big = max_nan(big, max_nan(fabsf(t), fabsf(u)));
+                const float2 a = make_float2(t * (1.0f - 0x1p-22f), u * (1.0f - 0x1p-22f));
+                const float2 b = make_float2(t * (1.0f + 0x1p-22f), u * (1.0f + 0x1p-22f));
+                lo = lo << 16 | (uint32_t)__nv_cvt_float2_to_fp8x2(a, __NV_SATFINITE, __NV_E4M3);
+                hi = hi << 16 | (uint32_t)__nv_cvt_float2_to_fp8x2(b, __NV_SATFINITE, __NV_E4M3);
+            }
+            same &= lo == hi;
+            w[f] = lo;
+        }
+        exact |= !same || big != big;
+    }
+    if (exact) {
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+            w[f] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[f] |= to_code<FMT>(x[4 * f + e], s, inv) << (8 * e);
+        }
+    }
+}
+
 // four codes moved from scale s0 to scale s1 (s1 > s0 >= 0)
 template <int FMT>
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float s0, float s1) {
@@ -99,7 +157,19 @@ __device__ __forceinline__ int table_row(const AppendParams& p, int t, int pos) 
     return -1;
 }
 
-constexpr int SLOTS = 4;  // slots of eight values per thread: 32 values in registers
+constexpr int SLOTS = 2;  // slots of eight values per thread
+
+// the largest value over the CTA, in every thread
+__device__ __forceinline__ float block_max(float a, float* red) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
+    __syncthreads();
+    a = (int)(threadIdx.x & 31) < (int)(blockDim.x >> 5) ? red[threadIdx.x & 31] : 0.0f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+    return a;
+}
 
 template <int D, int FMT, typename T, bool HALF>
 __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* red) {
@@ -110,7 +180,13 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
     // The sequence and block: sequence b owns the virtual blocks from
     // floor(cu[b] / block) + 2b on, at least as many as it can touch.
     int b = vb, t0 = vb, n = 1, j = 0;
-    if (p.cu) {
+    if (p.cu && c.batch == 1) {
+        b = 0;
+        t0 = p.cu[0];
+        n = p.cu[1] - t0;
+        j = vb - (t0 >> c.block_log2);
+        if (j < 0) return;
+    } else if (p.cu) {
         int upto = 0;
         for (int s = 0; s < c.batch; s += nt) {
             const int i = s + tid;
@@ -123,6 +199,8 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
         t0 = p.cu[b];
         n = p.cu[b + 1] - t0;
         j = vb - ((t0 >> c.block_log2) + 2 * b);
+    }
+    if (p.cu) {
         if (n <= 0 || t0 < 0 || t0 + n > p.tokens) {
             if (tid == 0 && (n < 0 || (n > 0 && (t0 < 0 || t0 + n > p.tokens)))) atomicOr(p.err, ERR_KV_RANGE);
             return;
@@ -139,14 +217,6 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
     if (start >= len) return;
     const int lo = max(start, first), hi = min(start + block, len);
     const int page = p.c.table[(long long)b * c.max_pages + (start >> c.page_log2)];
-    if ((unsigned)page >= (unsigned)c.n_pages) {
-        if (tid == 0) atomicOr(p.err, ERR_KV_RANGE);
-        return;
-    }
-    const long long slot = slot_base(c, page, h) + (start & ((1 << c.page_log2) - 1));
-    float* scale_at = (is_v ? c.vs : c.ks) + (slot >> c.block_log2);
-    uint8_t* codes = (is_v ? c.v : c.k) + slot * D;
-
     constexpr int SPT = D / 8;  // slots per token
     const T* src = reinterpret_cast<const T*>(is_v ? p.v : p.k);
     const long long stride = is_v ? p.v_stride : p.k_stride;
@@ -170,18 +240,31 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
                 rotate_slot<HALF>(x[i], p.cos + (long long)r * (rot >> 1), p.sin + (long long)r * (rot >> 1), sl);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float m = fabsf(x[i][e]);
-            if (m < INFINITY) a = fmaxf(a, m);
-        }
+        for (int e = 0; e < 8; ++e) a = fmaxf(a, fabsf(x[i][e]));  // NaN loses
     }
+    // (the page is looked at only now: its id was on the way while the rows were)
+    if ((unsigned)page >= (unsigned)c.n_pages) {
+        if (tid == 0) atomicOr(p.err, ERR_KV_RANGE);
+        return;
+    }
+    const long long slot = slot_base(c, page, h) + (start & ((1 << c.page_log2) - 1));
+    float* scale_at = (is_v ? c.vs : c.ks) + (slot >> c.block_log2);
+    uint8_t* codes = (is_v ? c.v : c.k) + slot * D;
+
     const float s_old = start >= first ? 0.0f : *scale_at;
+    a = block_max(a, red);
+    if (a == INFINITY) {  // an infinite value counts for nothing: the largest of the others
+        a = 0.0f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    if ((tid & 31) == 0) red[tid >> 5] = a;
-    __syncthreads();
-    a = red[0];
-    for (int w = 1; w < (nt >> 5); ++w) a = fmaxf(a, red[w]);
+        for (int i = 0; i < SLOTS; ++i) {
+            if (lo + (tid + i * nt) / SPT >= hi) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (fabsf(x[i][e]) < INFINITY) a = fmaxf(a, fabsf(x[i][e]));
+        }
+        __syncthreads();  // every thread has read the first maximum
+        a = block_max(a, red);
+    }
     const float s_new = fmaxf(s_old, __fdiv_rn(a, FMT == QG_KV8_INT8 ? 127.0f : 448.0f));
     const float inv = s_new > 0.0f ? __frcp_rn(s_new) : 0.0f;
 
@@ -210,12 +293,7 @@ __device__ __forceinline__ void kv_unit(const AppendParams& p, int unit, float* 
         int at, bt;
         slot_places<HALF>(sl, rot, at, bt);
         uint32_t w[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-            w[f] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[f] |= to_code<FMT>(x[i][4 * f + e], s_new, inv) << (8 * e);
-        }
+        to_codes<FMT>(x[i], s_new, inv, w);
         uint8_t* row = codes + (pos - start) * D;
         *reinterpret_cast<uint32_t*>(row + at) = w[0];
         *reinterpret_cast<uint32_t*>(row + bt) = w[1];
@@ -280,7 +358,7 @@ __device__ __forceinline__ void q_unit(const AppendParams& p, unsigned item) {
 }
 
 template <int D, int FMT, typename T, bool HALF>
-__global__ void append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(1024) append_kernel(const AppendParams p) {
     __shared__ float red[32];
     pdl_wait();
     pdl_launch_dependents();

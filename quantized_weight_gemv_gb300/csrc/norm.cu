@@ -5,10 +5,16 @@
 // u and h' are formed in place, h' is squared and summed, z is formed.  Bound by memory
 // for many rows (two reads, two writes) and by latency for a few: one load round, two
 // reductions, one store round.
-//   rows of up to 1024 values : one warp per row, no shared memory
-//   longer rows               : one CTA per row, 8 values a thread (32 above 8192 values)
+//   rows of up to 256 values : one warp per row, no shared memory
+//   longer rows              : one CTA per row, 8 values a thread in 32 registers, so that
+//                              2048 threads of an SM have their loads in flight; above 8192
+//                              values 32 a thread, h being read after the first reduction
 // VEC: 16-byte accesses of eight consecutive values (n a multiple of 8, everything 16-byte
 // aligned); otherwise the same loop takes single values, a warp's neighbours side by side.
+// Two rows to a CTA (twice the loads in flight, half the threads) was slower: 32.7 against
+// 26.8 us for 8191 x 2048 in bfloat16; so was a warp for rows of 512 and 1024 (21.4 and 36.8
+// against 19.1 and 25.9 us for 16384 of them), and a CTA that walks over rows with the next
+// one's loads in flight (35.9 us at 8191 x 2048: 40 registers do not hold both rows).
 #include "kv8.cuh"
 
 namespace qg {
@@ -54,16 +60,16 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     if constexpr (WARP) {
         return v;
     } else {
-        const int warps = blockDim.x >> 5;
-        if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+        const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) red[threadIdx.x >> 5] = v;
         __syncthreads();
-        v = (int)(threadIdx.x & 31) < warps ? red[threadIdx.x & 31] : 0.0f;
-        return warp_sum(v);
+        return warp_sum(lane < warps ? red[lane] : 0.0f);
     }
 }
 
+// IT chunks of eight values per thread
 template <typename T, typename R, bool VEC, int IT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParams p) {
+__global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC ? 2 : 1) norm_kernel(const NormParams p) {
     __shared__ float red[2][32];
     pdl_wait();
     pdl_launch_dependents();
@@ -71,7 +77,6 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
     const long long row = WARP ? (long long)blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.rows) return;
     const int n = p.n;
-    const T* y = reinterpret_cast<const T*>(p.y);
     const T* gate = reinterpret_cast<const T*>(p.gate);
     const T* wpost = reinterpret_cast<const T*>(p.w_post);
     const T* wpre = reinterpret_cast<const T*>(p.w_pre);
@@ -86,56 +91,49 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
     for (int i = 0; i < IT; ++i) {
         const int at = place(i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[i][e] = hv[i][e] = 0.0f;
-        if (at < n) {
-            if (y) load_chunk<VEC>(y + row * p.y_stride, at, step, n, a[i]);
-            load_chunk<VEC>(h, at, step, n, hv[i]);
+        for (int e = 0; e < 8; ++e) a[i][e] = 0.0f;
+        if (at < n && p.y) load_chunk<VEC>(reinterpret_cast<const T*>(p.y) + row * p.y_stride, at, step, n, a[i]);
+        if (IT == 1) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) hv[i][e] = 0.0f;
+            if (at < n) load_chunk<VEC>(h, at, step, n, hv[i]);
         }
     }
-    if (y) {
-        float r = 1.0f;
-        if (wpost) {
-            float s = 0.0f;
+    float r = 1.0f;
+    if (wpost) {
+        float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < IT; ++i)
+        for (int i = 0; i < IT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s = fmaf(a[i][e], a[i][e], s);
-            r = rsqrtf(row_sum<WARP>(s, red[0]) / (float)n + p.eps);
-        }
-#pragma unroll
-        for (int i = 0; i < IT; ++i) {
-            const int at = place(i);
-            if (at >= n) continue;
-            float c[8];
-            if (wpost) {
-                load_chunk<VEC>(wpost, at, step, n, c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a[i][e] = a[i][e] * r * (c[e] + p.w_offset);
-            }
-            if (gate) {
-                load_chunk<VEC>(gate + row * p.gate_stride, at, step, n, c);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a[i][e] *= c[e];
-            }
-        }
+            for (int e = 0; e < 8; ++e) s = fmaf(a[i][e], a[i][e], s);
+        r = rsqrtf(row_sum<WARP>(s, red[0]) / (float)n + p.eps);
     }
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < IT; ++i)
+    for (int i = 0; i < IT; ++i) {
+        const int at = place(i);
+        if (at >= n) continue;
+        float c[8];
+        if (IT > 1) load_chunk<VEC>(h, at, step, n, hv[i]);
+        if (wpost) {
+            load_chunk<VEC>(wpost, at, step, n, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[i][e] = a[i][e] * r * (c[e] + p.w_offset);
+        }
+        if (gate) {
+            load_chunk<VEC>(gate + row * p.gate_stride, at, step, n, c);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a[i][e] *= c[e];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            hv[i][e] = (hv[i][e] + a[i][e]) * p.res_scale;
-            s = fmaf(hv[i][e], hv[i][e], s);
+            a[i][e] = (hv[i][e] + a[i][e]) * p.res_scale;  // h'
+            s = fmaf(a[i][e], a[i][e], s);
         }
-    if (p.h_out) {
-        R* out = reinterpret_cast<R*>(p.h_out) + row * p.h_out_stride;
-#pragma unroll
-        for (int i = 0; i < IT; ++i)
-            if (place(i) < n) store_chunk<VEC>(out, place(i), step, n, hv[i]);
+        if (p.h_out) store_chunk<VEC>(reinterpret_cast<R*>(p.h_out) + row * p.h_out_stride, at, step, n, a[i]);
     }
     if (!wpre) return;
-    const float r = rsqrtf(row_sum<WARP>(s, red[1]) / (float)n + p.eps);
-    T* z = reinterpret_cast<T*>(p.z) + row * p.z_stride;
+    r = rsqrtf(row_sum<WARP>(s, red[1]) / (float)n + p.eps);
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int at = place(i);
@@ -143,18 +141,14 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) norm_kernel(const NormParam
         float c[8];
         load_chunk<VEC>(wpre, at, step, n, c);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) hv[i][e] = hv[i][e] * r * (c[e] + p.w_offset);
-        store_chunk<VEC>(z, at, step, n, hv[i]);
+        for (int e = 0; e < 8; ++e) a[i][e] = a[i][e] * r * (c[e] + p.w_offset);
+        store_chunk<VEC>(reinterpret_cast<T*>(p.z) + row * p.z_stride, at, step, n, a[i]);
     }
 }
 
 template <typename T, typename R, bool VEC>
 static int launch_rows(const NormParams& p, const LaunchCtx& lc) {
-    if (p.n <= 1024) {
-        const dim3 grid((unsigned)((p.rows + 3) / 4)), block(128);
-        return p.n <= 256 ? launch_kernel(norm_kernel<T, R, VEC, 1, true>, grid, block, 0, lc, p)
-                          : launch_kernel(norm_kernel<T, R, VEC, 4, true>, grid, block, 0, lc, p);
-    }
+    if (p.n <= 256) return launch_kernel(norm_kernel<T, R, VEC, 1, true>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, lc, p);
     const int per = p.n <= 8192 ? 8 : 32;
     const dim3 grid((unsigned)p.rows), block((unsigned)(((p.n + per - 1) / per + 31) & ~31));
     return per == 8 ? launch_kernel(norm_kernel<T, R, VEC, 1, false>, grid, block, 0, lc, p)
