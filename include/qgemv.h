@@ -428,12 +428,12 @@ int kv8_values(const qg_kv8_cache* cache, float* k_out, float* v_out, unsigned f
  *   Scores, sums and outputs are accumulated in fp32.  With fp32 rows, queries and
  *   weights enter the tensor cores as two binary16 pieces (22 bits); with 16-bit rows the
  *   weights are rounded to binary16 once.
- *   ws : device workspace of kv8_attention_workspace_bytes() bytes, 16-byte aligned, whose
- *     first QG_KV8_CTL_BYTES bytes are zero-filled once after allocation; every completed
- *     call leaves them zero.  Calls sharing a workspace must not overlap on the GPU.
+ *   ws : device workspace of kv8_attention_workspace_bytes() bytes, 16-byte aligned, no
+ *     initial content.  Calls sharing a workspace must not overlap on the GPU.
  *   The result does not depend on timing: sums are taken in a fixed order.
+ *   One or two launches: the second adds up what was split over the SMs, the first being
+ *   the only one where the page table holds at most 128 tokens per sequence.
  */
-#define QG_KV8_CTL_BYTES 4096
 
 typedef struct qg_kv8_attention_args {
     const void* q;

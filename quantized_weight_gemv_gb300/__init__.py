@@ -36,7 +36,6 @@ QG_DTYPE_F16 = 1
 QG_DTYPE_BF16 = 2
 QG_ROPE_HALF = 0
 QG_ROPE_INTERLEAVED = 1
-QG_KV8_CTL_BYTES = 4096
 QG_KV8_MAX_BATCH = 4096
 QG_MAX_NORM_N = 32768
 
@@ -637,8 +636,8 @@ def kv8_rope_append(cache, k, v, kv_len, cu_tokens=None, cos=None, sin=None, pos
 
 
 def kv8_workspace(head_dim, device) -> torch.Tensor:
-    """A zero-filled workspace for :func:`kv8_attention` (reusable; calls leave its control words zero)."""
-    return torch.zeros(int(lib().kv8_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
+    """A workspace for :func:`kv8_attention` (reusable; no initial content)."""
+    return torch.empty(int(lib().kv8_attention_workspace_bytes(head_dim)), dtype=torch.uint8, device=device)
 
 
 class KV8Attention(_Plan):

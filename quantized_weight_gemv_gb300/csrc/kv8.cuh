@@ -133,9 +133,10 @@ struct AttnParams {
     long long q_stride, out_stride;
     int tokens, hq, group, dtype, window;
     float scale, softcap;
-    // the workspace: arrival counters (zero between calls), and partials: (reference, sum) of
-    // each row, and the rows' weighted values
-    unsigned* counter;
+    int unit;  // token tiles of the smallest unit of work
+    // the workspace: the split row tiles by the CTA in which they begin, and partials: (reference,
+    // sum) of each row, and the rows' weighted values
+    int4* split;
     float* part_ml;
     float* part_o;
     unsigned* err;

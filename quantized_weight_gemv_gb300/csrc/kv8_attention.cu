@@ -4,8 +4,9 @@
 // list that the CTAs share out evenly on the device from kv_len and cu_tokens, so ragged
 // batches balance and nothing about the lengths has to be known on the host.  Each CTA
 // takes a contiguous run of the list; a row tile that falls into several CTAs leaves one
-// partial (running maximum, sum, weighted values) per CTA, and the CTA that arrives last
-// adds them up in order.  No CTA waits for another.
+// partial (running maximum, sum, weighted values) per CTA, and a second, small launch adds
+// them up in order.  No CTA waits for another.  (The CTA that arrives last adding them up,
+// 64 partials of 8 x 256 values for one token over 8191, took 8 us on its one SM.)
 //
 // Mathematics: scores are held in base 2 (x = l * log2 e).  A warp takes 16 cache tokens at
 // a time: S^T = K Q^T with the tokens as the 16 rows of mma.m16n8k16 and up to 8 query rows
@@ -29,6 +30,7 @@ constexpr int SUB = 16;         // cache tokens per warp step
 // 64 rows over 8192, one sequence: 35 / 39; 128 rows 46 / 41; 512 rows 130 / 63.
 constexpr int PREFILL_ROWS = 64;
 constexpr int MAX_CTAS = 320;   // CTAs that share out one call (workspace slots)
+constexpr size_t SPLIT_BYTES = 8192;  // the workspace's list of split row tiles
 
 // ---------------------------------------------------------------- device helpers
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -66,9 +68,7 @@ template <int D, int NT>
 struct Shape {
     static constexpr int RT = 8 * NT;                 // query rows per tile
     static constexpr int QUADS = D * NT / 16;         // groups of four values (per lane) of a row tile's output
-    // the warps' shares of a row tile, or the (reference, sum) pairs of its partials
-    static constexpr size_t merge_bytes = (size_t)W * RT * D * 4 > (size_t)MAX_CTAS * RT * 8 ? (size_t)W * RT * D * 4
-                                                                                             : (size_t)MAX_CTAS * RT * 8;
+    static constexpr size_t merge_bytes = (size_t)W * RT * D * 4;  // the warps' shares of a row tile
 };
 
 // One quad of the output: lane (g, t) holds d..d+3 of one column of the row tile.
@@ -97,25 +97,26 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
     __shared__ float row_factor[RT];                 // 2^e * scale (* log2 e, or / softcap)
     __shared__ float wm[W][RT], wl[W][RT], wv[W];    // per warp: reference, sum, value-scale reference
     __shared__ float tile_m[RT], tile_l[RT];
-    __shared__ long long wsum[W];
-    __shared__ int last_s;
-    long long* ends = reinterpret_cast<long long*>(smem);  // before the first row tile, then kept past the merge area
-    float* merge = reinterpret_cast<float*>(smem + (((size_t)p.c.batch * 8 + 15) & ~(size_t)15));
+    __shared__ unsigned wsum[W];
+    __shared__ int row_tok[RT], row_head[RT];        // a row's token (within its sequence) and query head
+    unsigned* ends = reinterpret_cast<unsigned*>(smem);
+    float* merge = reinterpret_cast<float*>(smem + (((size_t)p.c.batch * 4 + 15) & ~(size_t)15));
 
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, g = lane >> 2, t = lane & 3;
     pdl_wait();
     pdl_launch_dependents();
 
-    // Prefix sums of the sequences' units.  A unit is one token tile while the list is long;
-    // a list of at most four tiles per CTA is cut into units of 1, 2 or 4 tiles, the first
-    // that gives every CTA at most one unit: no CTA then starts a second row tile, whose
-    // fixed costs are several tiles' worth.
-    long long total = 0;
-    int unit = 1;
+    // Prefix sums of the sequences' units.  A unit is p.unit token tiles (one, but for caches
+    // whose list would pass 2^30) while the list is long; a list of at most four units per
+    // CTA is cut into units of twice and four times that, the first that gives every CTA at
+    // most one: no CTA then starts a second row tile, whose fixed costs are several tiles'
+    // worth.
+    unsigned total = 0;
+    int unit = p.unit;
     const SeqInfo only = seq_info<RT>(p, 0);  // a lone sequence is looked up once
     auto units_of = [&](int b) {
         const SeqInfo si = p.c.batch == 1 ? only : seq_info<RT>(p, b);
-        return (long long)p.c.hkv * si.qt * ((si.nt + unit - 1) / unit);
+        return (unsigned)(p.c.hkv * si.qt * ((si.nt + unit - 1) / unit));
     };
     while (true) {
         total = 0;
@@ -123,15 +124,15 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             total = units_of(0);
         } else {
             for (int s = 0; s < p.c.batch; s += W * 32) {
-                long long u = s + tid < p.c.batch ? units_of(s + tid) : 0;
+                unsigned u = s + tid < p.c.batch ? units_of(s + tid) : 0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long v = __shfl_up_sync(0xffffffffu, u, o);
+                    const unsigned v = __shfl_up_sync(0xffffffffu, u, o);
                     if (lane >= o) u += v;
                 }
                 if (lane == 31) wsum[w] = u;
                 __syncthreads();
-                long long base = total;
+                unsigned base = total;
                 for (int i = 0; i < W; ++i) {
                     if (i < w) base += wsum[i];
                     total += wsum[i];
@@ -140,16 +141,21 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                 __syncthreads();
             }
         }
-        if (total <= gridDim.x) break;
-        if (unit == 1 && total > 4ll * gridDim.x) break;
-        if (unit == 4) break;  // one more cut would idle half the CTAs: as it is
+        if (total <= gridDim.x || total > 4 * gridDim.x || unit == 4 * p.unit) break;
         unit *= 2;
     }
-    const long long ctas = min((long long)gridDim.x, total);
+    const unsigned ctas = min(gridDim.x, total);
+    if (tid == 0) p.split[blockIdx.x].x = -1;  // until a row tile that begins here is found to go on
     if (blockIdx.x >= ctas) return;
-    long long pos = total * blockIdx.x / ctas;
-    const long long end = total * (blockIdx.x + 1) / ctas;
-    const long long my_start = pos;
+    // CTA c takes units c * each + min(c, more) on, `each` or one more of them
+    const unsigned each = total / ctas, more = total % ctas;
+    auto first_unit = [&](unsigned c) { return c * each + min(c, more); };
+    auto cta_of = [&](unsigned u) {
+        const unsigned big = more * (each + 1);
+        return u < big ? u / (each + 1) : more + (u - big) / each;
+    };
+    unsigned pos = first_unit(blockIdx.x);
+    const unsigned end = first_unit(blockIdx.x + 1), my_start = pos;
 
     while (pos < end) {
         // the sequence of this unit, its row tile and the run of units taken here
@@ -165,11 +171,11 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             }
         }
         const SeqInfo si = p.c.batch == 1 ? only : seq_info<RT>(p, b);
-        const long long base = b ? ends[b - 1] : 0;
+        const unsigned base = b ? ends[b - 1] : 0;
         const int nu = (si.nt + unit - 1) / unit;  // units of a row tile
         const int seg = (int)((pos - base) / nu), unit0 = (int)((pos - base) % nu);
-        const int count = (int)min((long long)(nu - unit0), end - pos);
-        const long long seg_start = pos - unit0;
+        const int count = min(nu - unit0, (int)(end - pos));
+        const unsigned seg_start = pos - unit0;
         const int h = seg / si.qt, qt = seg % si.qt;
 
         const int rows = min(RT, si.n * p.group - qt * RT);
@@ -179,6 +185,28 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
         const int hi_min = at0, hi_max = at1;
         const int lo_min = p.window > 0 ? max(0, at0 - p.window + 1) : 0;
         const int lo_max = p.window > 0 ? max(0, at1 - p.window + 1) : 0;
+
+        // ---- the tile's queries, row w (+ W) per warp: requested before anything else
+        constexpr int PER = D / 32;  // values per lane, consecutive
+        static_assert(RT == NT * W, "a row per warp and row tile of 8");
+        float xq[NT][PER];
+        int tok_of[NT], head_of[NT];
+#pragma unroll
+        for (int cw = 0; cw < NT; ++cw) {
+            const int r = qt * RT + w + cw * W, i = r / p.group, hh = h * p.group + r - i * p.group;
+            tok_of[cw] = i, head_of[cw] = hh;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) xq[cw][e] = 0.0f;
+            if (w + cw * W < rows) {
+                const long long at = (si.t0 + i) * p.q_stride + (long long)hh * D + lane * PER;
+                if constexpr (PIECES == 2)
+                    load_values(reinterpret_cast<const float*>(p.q) + at, xq[cw]);
+                else if (p.dtype == QG_DTYPE_F16)
+                    load_values(reinterpret_cast<const __half*>(p.q) + at, xq[cw]);
+                else
+                    load_values(reinterpret_cast<const __nv_bfloat16*>(p.q) + at, xq[cw]);
+            }
+        }
 
         // ---- cache tokens, 16 per step: steps first + w, + W, ... of this run's tiles
         const int origin = hi_max < 0 ? 0 : lo_min & ~(SUB - 1);
@@ -227,25 +255,12 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
             load_k(s);
             load_v(s);
         }
-        // ---- the tile's queries
+        // ---- the queries' pieces, in the order the matrix instructions read them
         __syncthreads();  // the previous row tile's shared arrays are no longer read
-        for (int col = w; col < RT; col += W) {
-            const int r = qt * RT + col;
-            const bool valid = col < rows;
-            const int i = valid ? r / p.group : 0, hh = h * p.group + (valid ? r % p.group : 0);
-            constexpr int PER = D / 32;  // values per lane, consecutive
-            float x[PER];
 #pragma unroll
-            for (int e = 0; e < PER; ++e) x[e] = 0.0f;
-            if (valid) {
-                const long long at = (si.t0 + i) * p.q_stride + (long long)hh * D + lane * PER;
-                if constexpr (PIECES == 2)
-                    load_values(reinterpret_cast<const float*>(p.q) + at, x);
-                else if (p.dtype == QG_DTYPE_F16)
-                    load_values(reinterpret_cast<const __half*>(p.q) + at, x);
-                else
-                    load_values(reinterpret_cast<const __nv_bfloat16*>(p.q) + at, x);
-            }
+        for (int cw = 0; cw < NT; ++cw) {
+            const int col = w + cw * W;
+            float(&x)[PER] = xq[cw];
             float a = 0.0f;
 #pragma unroll
             for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[e]));
@@ -265,6 +280,10 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                     reinterpret_cast<uint32_t*>(&qf[PIECES - 1][col >> 3][ks][ln])[rg] =
                         half2_bits(u - __low2float(hi2), v - __high2float(hi2));
             }
+            if (lane == 0) {
+                row_tok[col] = tok_of[cw];
+                row_head[col] = head_of[cw];
+            }
             if (lane == 0)
                 row_factor[col] = ldexpf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f, ex);
         }
@@ -282,7 +301,7 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                 mo[n][i] = -1e30f;
                 l[n][i] = 0.0f;
                 rf[n][i] = row_factor[col];
-                const int at = si.len - si.n + (qt * RT + col) / p.group;
+                const int at = si.len - si.n + row_tok[col];
                 hi_c[n][i] = at;
                 lo_c[n][i] = p.window > 0 ? at - p.window + 1 : 0;
             }
@@ -470,13 +489,10 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
         // a run that continues the previous CTA's row tile goes to its first slot, one that
         // the next CTA continues to its second
         const int slot_id = 2 * blockIdx.x + (seg_start >= my_start ? 1 : 0);
-        auto write_row = [&](int quad, float4 v) {
-            int n, col, d;
-            quad_place<D>(quad, lane, n, col, d);
+        auto write_row = [&](int col, int d, float4 v) {
             const float sum = tile_l[col];
             const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-            const int r = qt * RT + col;
-            const long long at = (long long)(si.t0 + r / p.group) * p.out_stride + (long long)(h * p.group + r % p.group) * D + d;
+            const long long at = (long long)(si.t0 + row_tok[col]) * p.out_stride + (long long)row_head[col] * D + d;
             const float x[4] = {v.x * inv, v.y * inv, v.z * inv, v.w * inv};
             if constexpr (PIECES == 2)
                 store4(reinterpret_cast<float*>(p.out) + at, x);
@@ -484,14 +500,6 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                 store4(reinterpret_cast<__half*>(p.out) + at, x);
             else
                 store4(reinterpret_cast<__nv_bfloat16*>(p.out) + at, x);
-        };
-        auto write_lse = [&]() {
-            if (p.lse && tid < rows) {
-                const int r = qt * RT + tid;
-                const float sum = tile_l[tid];
-                p.lse[(long long)(si.t0 + r / p.group) * p.hq + h * p.group + r % p.group] =
-                    sum == 0.0f ? -INFINITY : (tile_m[tid] + log2f(sum)) * 0.693147180559945f;
-            }
         };
         for (int quad = w; quad < S::QUADS; quad += W) {
             int n, col, d;
@@ -505,94 +513,120 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
                 acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
             }
             if (whole)
-                write_row(quad, acc);
+                write_row(col, d, acc);
             else
-                reinterpret_cast<float4*>(p.part_o)[((size_t)slot_id * S::QUADS + quad) * 32 + lane] = acc;
+                *reinterpret_cast<float4*>(p.part_o + ((size_t)slot_id * RT + col) * D + d) = acc;
         }
         if (whole) {
-            write_lse();
+            if (p.lse && tid < rows)
+                p.lse[(long long)(si.t0 + row_tok[tid]) * p.hq + row_head[tid]] =
+                    tile_l[tid] == 0.0f ? -INFINITY : (tile_m[tid] + log2f(tile_l[tid])) * 0.693147180559945f;
         } else {
-            if (tid < RT) {
-                p.part_ml[((size_t)slot_id * RT + tid) * 2] = tile_m[tid];
-                p.part_ml[((size_t)slot_id * RT + tid) * 2 + 1] = tile_l[tid];
-            }
-            // the CTAs of this row tile: those that hold its first and its last unit
-            const int c0 = (int)(((seg_start + 1) * ctas - 1) / total);
-            const int c1 = (int)(((seg_start + nu) * ctas - 1) / total);
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                unsigned prev;
-                asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(prev) : "l"(p.counter + c0) : "memory");
-                last_s = prev == (unsigned)(c1 - c0);
-                if (last_s) p.counter[c0] = 0u;  // every CTA of the row tile has arrived
-            }
-            __syncthreads();
-            if (last_s) {
-                __threadfence();
-                auto slot_of_cta = [&](int c) {
-                    return (size_t)(2 * c + (c == c0 ? 1 : 0));  // only c0 begins the row tile
-                };
-                // (reference, sum) of every partial side by side, then a warp per row
-                const int parts = c1 - c0 + 1;
-                float2* ml = reinterpret_cast<float2*>(merge);
-                for (int i = tid; i < parts * RT; i += W * 32)
-                    ml[i] = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + slot_of_cta(c0 + i / RT) * RT + i % RT);
-                __syncthreads();
-                for (int col = w; col < RT; col += W) {
-                    float m = -1e30f, sum = 0.0f;
-                    for (int i = lane; i < parts; i += 32) m = fmaxf(m, ml[i * RT + col].x);
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-                    for (int i = lane; i < parts; i += 32) {
-                        const float f = ex2(ml[i * RT + col].x - m);
-                        sum += ml[i * RT + col].y * f;
-                        ml[i * RT + col].x = f;  // now the partial's factor
-                    }
-                    sum = warp_sum(sum);
-                    if (lane == 0) {
-                        tile_m[col] = m;
-                        tile_l[col] = sum;
-                    }
-                }
-                __syncthreads();
-                for (int quad = w; quad < S::QUADS; quad += W) {
-                    int n, col, d;
-                    quad_place<D>(quad, lane, n, col, d);
-                    if (col >= rows) continue;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    const float4* at = reinterpret_cast<const float4*>(p.part_o) + (size_t)quad * 32 + lane;
-#pragma unroll 8
-                    for (int i = 0; i < parts; ++i) {
-                        const float4 v = __ldcg(at + slot_of_cta(c0 + i) * S::QUADS * 32);
-                        const float f = ml[i * RT + col].x;
-                        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-                    }
-                    write_row(quad, acc);
-                }
-                write_lse();
-            }
+            if (tid < rows) reinterpret_cast<float2*>(p.part_ml)[(size_t)slot_id * RT + tid] = make_float2(tile_m[tid], tile_l[tid]);
+            // it begins here: the CTA of its last unit, and which rows it holds
+            if (tid == 0 && seg_start >= my_start)
+                p.split[blockIdx.x] = make_int4((int)cta_of(seg_start + nu - 1), si.t0, qt * RT, h << 5 | rows);
         }
         pos += count;
     }
 }
 
+// The partials of split row tiles added up in order: one CTA per (CTA in which such a tile
+// begins, row), the threads sharing out the partials of each group of four values.
+constexpr int MERGE_THREADS = 128;
+template <int D, int RT, typename T>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_split_kernel(const AttnParams p) {
+    __shared__ float factor[MAX_CTAS], red[2][MERGE_THREADS / 32];
+    __shared__ float4 shares[MERGE_THREADS];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int c0 = blockIdx.x, col = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int4 split = p.split[c0];
+    const int rows = split.w & 31, h = split.w >> 5;
+    if (split.x < 0 || col >= rows) return;
+    const int parts = split.x - c0 + 1;
+    // only c0 holds the tile's first slot, the others continue it
+    auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * RT + col; };
+    constexpr int PER = (MAX_CTAS + MERGE_THREADS - 1) / MERGE_THREADS;
+    float2 ml[PER];
+    float m = -1e30f, sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = tid + k * MERGE_THREADS;
+        ml[k] = i < parts ? reinterpret_cast<const float2*>(p.part_ml)[row_of(i)] : make_float2(-1e30f, 0.0f);
+        m = fmaxf(m, ml[k].x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[0][w] = m;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, red[0][i]);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int i = tid + k * MERGE_THREADS;
+        const float f = ex2(ml[k].x - m);
+        sum = fmaf(ml[k].y, f, sum);
+        if (i < parts) factor[i] = f;
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) red[1][w] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < MERGE_THREADS / 32; ++i) sum += red[1][i];
+
+    constexpr int GROUPS = MERGE_THREADS / (D / 4);
+    const int d = tid % (D / 4) * 4;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = tid / (D / 4); i < parts; i += GROUPS) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part_o + row_of(i) * D + d);
+        const float f = factor[i];
+        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+    }
+    shares[tid] = acc;
+    __syncthreads();
+    if (tid >= D / 4) return;
+#pragma unroll
+    for (int i = 1; i < GROUPS; ++i) {
+        const float4 v = shares[i * (D / 4) + tid];
+        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+    const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+    const int r = split.z + col, i = r / p.group, hh = h * p.group + r - i * p.group;
+    store4(reinterpret_cast<T*>(p.out) + (split.y + (long long)i) * p.out_stride + (long long)hh * D + d, x);
+    if (p.lse && tid == 0)
+        p.lse[(split.y + (long long)i) * p.hq + hh] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+}
+
 template <int D, int FMT, int PIECES, int NT>
 static int launch_nt(AttnParams& p, unsigned char* ws, const LaunchCtx& lc) {
     using S = Shape<D, NT>;
-    p.counter = reinterpret_cast<unsigned*>(ws);
-    p.part_ml = reinterpret_cast<float*>(ws + QG_KV8_CTL_BYTES);
+    p.split = reinterpret_cast<int4*>(ws);
+    p.part_ml = reinterpret_cast<float*>(ws + SPLIT_BYTES);
     p.part_o = p.part_ml + (size_t)2 * MAX_CTAS * S::RT * 2;
-    const size_t smem = (((size_t)p.c.batch * 8 + 15) & ~(size_t)15) + S::merge_bytes;
+    const size_t smem = (((size_t)p.c.batch * 4 + 15) & ~(size_t)15) + S::merge_bytes;
     const void* kernel = reinterpret_cast<const void*>(attention_kernel<D, FMT, PIECES, NT>);
-    const int rc = ensure_smem_attr(kernel, smem, lc);
+    // opted in for every size: with the static arrays a dynamic part below 48 KB can pass that too
+    int rc = ensure_smem_attr(kernel, max(smem, (size_t)48 * 1024 + 1), lc);
     if (rc != QG_OK) return rc;
     // no more CTAs than resident at once, nor than there can be units
     const long long tiles = (((long long)p.c.max_pages << p.c.page_log2) + W * SUB - 1) / (W * SUB);
-    const long long qt = (long long)p.tokens * p.group / S::RT + p.c.batch;
-    const long long grid = min(min((long long)MAX_CTAS, (long long)lc.sm_count * (D * NT <= 128 ? 2 : 1)),
-                               p.c.hkv * qt * tiles);
-    return launch_kernel(attention_kernel<D, FMT, PIECES, NT>, dim3((unsigned)grid), dim3(W * 32), smem, lc, p);
+    const long long row_tiles = p.c.hkv * ((long long)p.tokens * p.group / S::RT + p.c.batch);
+    if (row_tiles > (1ll << 30)) return QG_ERR_UNSUPPORTED;
+    p.unit = 1;
+    while (row_tiles * ((tiles + p.unit - 1) / p.unit) > (1ll << 30)) p.unit *= 2;
+    const unsigned grid = (unsigned)min((long long)min(MAX_CTAS, lc.sm_count * (D * NT <= 128 ? 2 : 1)), row_tiles * tiles);
+    rc = launch_kernel(attention_kernel<D, FMT, PIECES, NT>, dim3(grid), dim3(W * 32), smem, lc, p);
+    // a cache of one token tile per sequence leaves nothing split
+    if (rc != QG_OK || tiles == 1) return rc;
+    const dim3 rows(grid, S::RT);
+    if (PIECES == 2) return launch_kernel(merge_split_kernel<D, S::RT, float>, rows, dim3(MERGE_THREADS), 0, lc, p);
+    return p.dtype == QG_DTYPE_F16
+               ? launch_kernel(merge_split_kernel<D, S::RT, __half>, rows, dim3(MERGE_THREADS), 0, lc, p)
+               : launch_kernel(merge_split_kernel<D, S::RT, __nv_bfloat16>, rows, dim3(MERGE_THREADS), 0, lc, p);
 }
 
 template <int D, int FMT, int PIECES>
@@ -618,7 +652,8 @@ static int launch_d(AttnParams& p, int d, unsigned char* ws, const LaunchCtx& lc
 
 size_t kv8_ws_bytes(int d) {
     using namespace kv8;
-    return max(QG_KV8_CTL_BYTES + (size_t)2 * MAX_CTAS * 16 * (d + 2) * 4, prefill_ws_bytes(d));
+    static_assert(MAX_CTAS * sizeof(int4) <= SPLIT_BYTES, "list of split row tiles");
+    return max(SPLIT_BYTES + (size_t)2 * MAX_CTAS * 16 * (d + 2) * 4, prefill_ws_bytes(d));
 }
 
 int launch_kv8_attention(const qg_kv8_cache& c, const qg_kv8_attention_args& a, unsigned char* ws, const LaunchCtx& lc) {

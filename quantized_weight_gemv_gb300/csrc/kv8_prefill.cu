@@ -860,7 +860,7 @@ static int launch_shape(AttnParams p, unsigned char* ws, const LaunchCtx& lc) {
     if (tiles > 0x7fffffffll || p.c.hkv > 65535) return QG_ERR_UNSUPPORTED;
     // too few row tiles for the SMs: each one's token tiles are shared out
     const long long splits = min(32ll, max(1ll, (long long)min(PF_SLOTS, lc.sm_count) / (tiles * p.c.hkv)));
-    p.part_ml = reinterpret_cast<float*>(ws + QG_KV8_CTL_BYTES);
+    p.part_ml = reinterpret_cast<float*>(ws);
     p.part_o = p.part_ml + (size_t)PF_SLOTS * RR * 2;
     rc = launch_kernel(prefill_kernel<D, FMT, PIECES>, dim3((unsigned)tiles, (unsigned)p.c.hkv, (unsigned)splits),
                        dim3(PF_THREADS), C::smem, lc, p);
@@ -883,7 +883,7 @@ static int launch_d(const AttnParams& p, int d, unsigned char* ws, const LaunchC
     }
 }
 
-size_t prefill_ws_bytes(int d) { return QG_KV8_CTL_BYTES + (size_t)PF_SLOTS * (d == 256 ? 128 : 256) * (d + 2) * 4; }
+size_t prefill_ws_bytes(int d) { return (size_t)PF_SLOTS * (d == 256 ? 128 : 256) * (d + 2) * 4; }
 
 int launch_prefill(const AttnParams& p, int format, int d, unsigned char* ws, const LaunchCtx& lc) {
     const bool f32 = p.dtype == QG_DTYPE_F32;

@@ -193,7 +193,6 @@ def check_attention(s, dtype, hq, window=0, softcap=0.0, scale=None, use_cu=True
     got = plan.run().clone()
     for _ in range(runs - 1):
         assert torch.equal(plan.run(), got), "a second run differs"
-    assert int(plan.keep[-1][:qg.QG_KV8_CTL_BYTES].count_nonzero()) == 0
     held = np.abs(np.where(np.isfinite(kv[1]), kv[1], 0.0))
     top = max(held[np.asarray(s.table[b])[np.arange(f + n) // s.page], :, np.arange(f + n) % s.page].max()
               for b, (f, n) in enumerate(zip(s.first, s.new)) if n)
