@@ -531,74 +531,90 @@ __global__ void __launch_bounds__(W * 32, D * NT <= 128 ? 2 : 1) attention_kerne
     }
 }
 
-// The partials of split row tiles added up in order: one CTA per (CTA in which such a tile
-// begins, row), the threads sharing out the partials of each group of four values.
-constexpr int MERGE_THREADS = 128;
-template <int D, int RT, typename T>
-__global__ void __launch_bounds__(MERGE_THREADS) merge_split_kernel(const AttnParams p) {
+// The partials of split row tiles added up in order: a CTA per row and `span` CTAs of the
+// first launch, for each in which such a tile begins; the threads share out the partials of
+// each group of four values, so that the loads are a round or two deep.
+template <int D, int RT, int MERGE_THREADS, typename T>
+__global__ void __launch_bounds__(MERGE_THREADS) merge_split_kernel(const AttnParams p, int ctas, int span) {
     __shared__ float factor[MAX_CTAS], red[2][MERGE_THREADS / 32];
     __shared__ float4 shares[MERGE_THREADS];
     pdl_wait();
     pdl_launch_dependents();
-    const int c0 = blockIdx.x, col = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-    const int4 split = p.split[c0];
-    const int rows = split.w & 31, h = split.w >> 5;
-    if (split.x < 0 || col >= rows) return;
-    const int parts = split.x - c0 + 1;
-    // only c0 holds the tile's first slot, the others continue it
-    auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * RT + col; };
-    constexpr int PER = (MAX_CTAS + MERGE_THREADS - 1) / MERGE_THREADS;
-    float2 ml[PER];
-    float m = -1e30f, sum = 0.0f;
+    const int col = blockIdx.y, tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+    const int first = blockIdx.x * span, mine = first + lane;
+    const int4 entry = lane < span && mine < ctas ? p.split[mine] : make_int4(-1, 0, 0, 0);
+    constexpr int PER = (MAX_CTAS + MERGE_THREADS - 1) / MERGE_THREADS;  // partials per thread
+    for (unsigned todo = __ballot_sync(0xffffffffu, entry.x >= 0 && col < (entry.w & 31)); todo; todo &= todo - 1) {
+        const int from = __ffs(todo) - 1, c0 = first + from;
+        const int4 split = make_int4(__shfl_sync(0xffffffffu, entry.x, from), __shfl_sync(0xffffffffu, entry.y, from),
+                                     __shfl_sync(0xffffffffu, entry.z, from), __shfl_sync(0xffffffffu, entry.w, from));
+        const int h = split.w >> 5, parts = split.x - c0 + 1;
+        // only c0 holds the tile's first slot, the others continue it
+        auto row_of = [&](int i) { return (size_t)(2 * (c0 + i) + (i == 0 ? 1 : 0)) * RT + col; };
+        float2 ml[PER];
+        float m = -1e30f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int i = tid + k * MERGE_THREADS;
-        ml[k] = i < parts ? reinterpret_cast<const float2*>(p.part_ml)[row_of(i)] : make_float2(-1e30f, 0.0f);
-        m = fmaxf(m, ml[k].x);
-    }
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + k * MERGE_THREADS;
+            ml[k] = i < parts ? reinterpret_cast<const float2*>(p.part_ml)[row_of(i)] : make_float2(-1e30f, 0.0f);
+            m = fmaxf(m, ml[k].x);
+        }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[0][w] = m;
-    __syncthreads();
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        __syncthreads();  // the row before is done with the shared arrays
+        if (lane == 0) red[0][w] = m;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, red[0][i]);
+        for (int i = 0; i < MERGE_THREADS / 32; ++i) m = fmaxf(m, red[0][i]);
+        float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int i = tid + k * MERGE_THREADS;
-        const float f = ex2(ml[k].x - m);
-        sum = fmaf(ml[k].y, f, sum);
-        if (i < parts) factor[i] = f;
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) red[1][w] = sum;
-    __syncthreads();
-    sum = 0.0f;
+        for (int k = 0; k < PER; ++k) {
+            const int i = tid + k * MERGE_THREADS;
+            const float f = ex2(ml[k].x - m);
+            sum = fmaf(ml[k].y, f, sum);
+            if (i < parts) factor[i] = f;
+        }
+        sum = warp_sum(sum);
+        if (lane == 0) red[1][w] = sum;
+        __syncthreads();
+        sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < MERGE_THREADS / 32; ++i) sum += red[1][i];
+        for (int i = 0; i < MERGE_THREADS / 32; ++i) sum += red[1][i];
 
-    constexpr int GROUPS = MERGE_THREADS / (D / 4);
-    const int d = tid % (D / 4) * 4;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        constexpr int GROUPS = MERGE_THREADS / (D / 4);
+        const int d = tid % (D / 4) * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
-    for (int i = tid / (D / 4); i < parts; i += GROUPS) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part_o + row_of(i) * D + d);
-        const float f = factor[i];
-        acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
-    }
-    shares[tid] = acc;
-    __syncthreads();
-    if (tid >= D / 4) return;
+        for (int i = tid / (D / 4); i < parts; i += GROUPS) {
+            const float4 v = *reinterpret_cast<const float4*>(p.part_o + row_of(i) * D + d);
+            const float f = factor[i];
+            acc.x += v.x * f, acc.y += v.y * f, acc.z += v.z * f, acc.w += v.w * f;
+        }
+        shares[tid] = acc;
+        __syncthreads();
+        if (tid >= D / 4) continue;
 #pragma unroll
-    for (int i = 1; i < GROUPS; ++i) {
-        const float4 v = shares[i * (D / 4) + tid];
-        acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        for (int i = 1; i < GROUPS; ++i) {
+            const float4 v = shares[i * (D / 4) + tid];
+            acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+        }
+        const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
+        const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
+        const int r = split.z + col, i = r / p.group, hh = h * p.group + r - i * p.group;
+        store4(reinterpret_cast<T*>(p.out) + (split.y + (long long)i) * p.out_stride + (long long)hh * D + d, x);
+        if (p.lse && tid == 0)
+            p.lse[(split.y + (long long)i) * p.hq + hh] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
     }
-    const float inv = sum > 0.0f ? 1.0f / sum : (sum == 0.0f ? 0.0f : sum);
-    const float x[4] = {acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv};
-    const int r = split.z + col, i = r / p.group, hh = h * p.group + r - i * p.group;
-    store4(reinterpret_cast<T*>(p.out) + (split.y + (long long)i) * p.out_stride + (long long)hh * D + d, x);
-    if (p.lse && tid == 0)
-        p.lse[(split.y + (long long)i) * p.hq + hh] = sum == 0.0f ? -INFINITY : (m + log2f(sum)) * 0.693147180559945f;
+}
+
+template <int D, int RT, typename T>
+static int launch_merge(const AttnParams& p, unsigned ctas, long long row_tiles, const LaunchCtx& lc) {
+    const unsigned rows = p.cu ? RT : (unsigned)min(RT, p.group);  // the most that a row tile can hold
+    // Few row tiles are split over many CTAs, few of which hold the beginning of one: many
+    // threads each; else about as many beginnings as CTAs, with few partials.
+    if (row_tiles * 4 <= ctas)
+        return launch_kernel(merge_split_kernel<D, RT, 512, T>, dim3((ctas + 7) / 8, rows), dim3(512), 0, lc, p, (int)ctas, 8);
+    return launch_kernel(merge_split_kernel<D, RT, 128, T>, dim3(ctas, rows), dim3(128), 0, lc, p, (int)ctas, 1);
 }
 
 template <int D, int FMT, int PIECES, int NT>
@@ -622,11 +638,9 @@ static int launch_nt(AttnParams& p, unsigned char* ws, const LaunchCtx& lc) {
     rc = launch_kernel(attention_kernel<D, FMT, PIECES, NT>, dim3(grid), dim3(W * 32), smem, lc, p);
     // a cache of one token tile per sequence leaves nothing split
     if (rc != QG_OK || tiles == 1) return rc;
-    const dim3 rows(grid, S::RT);
-    if (PIECES == 2) return launch_kernel(merge_split_kernel<D, S::RT, float>, rows, dim3(MERGE_THREADS), 0, lc, p);
-    return p.dtype == QG_DTYPE_F16
-               ? launch_kernel(merge_split_kernel<D, S::RT, __half>, rows, dim3(MERGE_THREADS), 0, lc, p)
-               : launch_kernel(merge_split_kernel<D, S::RT, __nv_bfloat16>, rows, dim3(MERGE_THREADS), 0, lc, p);
+    if (PIECES == 2) return launch_merge<D, S::RT, float>(p, grid, row_tiles, lc);
+    return p.dtype == QG_DTYPE_F16 ? launch_merge<D, S::RT, __half>(p, grid, row_tiles, lc)
+                                   : launch_merge<D, S::RT, __nv_bfloat16>(p, grid, row_tiles, lc);
 }
 
 template <int D, int FMT, int PIECES>
