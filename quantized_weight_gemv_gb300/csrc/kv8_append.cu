@@ -393,27 +393,38 @@ static int launch_t(const AppendParams& p, int d, bool half, const LaunchCtx& lc
     }
 }
 
-// The values that the codes stand for: 16 codes a thread, grid.y 0 for keys and 1 for values.
+// The values that the codes stand for: four words of four codes a thread, neighbours side by
+// side in each (16 consecutive codes a thread wrote half sectors: 9.7 us for a pool of 8.5 M
+// codes), grid.y 0 for keys and 1 for values.
+constexpr int VALUE_WORDS = 4;
 template <int FMT>
-__global__ void values_kernel(const CacheView c, float* k_out, float* v_out, long long vecs, int d_log2) {
+__global__ void __launch_bounds__(256) values_kernel(const CacheView c, float* k_out, float* v_out, long long words, int d_log2) {
     pdl_wait();
     pdl_launch_dependents();
-    const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
     float* out = blockIdx.y ? v_out : k_out;
-    if (i >= vecs || !out) return;
-    const uint4 w = reinterpret_cast<const uint4*>(blockIdx.y ? c.v : c.k)[i];
-    const float s = (blockIdx.y ? c.vs : c.ks)[(i << 4 >> d_log2) >> c.block_log2];
-    const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+    if (!out) return;
+    const uint32_t* codes = reinterpret_cast<const uint32_t*>(blockIdx.y ? c.v : c.k);
+    const float* scales = blockIdx.y ? c.vs : c.ks;
+    const long long first = (long long)blockIdx.x * (256 * VALUE_WORDS) + threadIdx.x;
+    uint32_t w[VALUE_WORDS];
+    float s[VALUE_WORDS];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < VALUE_WORDS; ++j) {
+        const long long i = first + j * 256;
+        w[j] = i < words ? codes[i] : 0u;
+        s[j] = i < words ? scales[(i << 2 >> d_log2) >> c.block_log2] : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < VALUE_WORDS; ++j) {
+        const long long i = first + j * 256;
         float x[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            const uint32_t b = (ws[j] >> (8 * e)) & 255u;
-            x[e] = s * (FMT == QG_KV8_INT8 ? (float)(int8_t)b
-                                           : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3))));
+            const uint32_t b = (w[j] >> (8 * e)) & 255u;
+            x[e] = s[j] * (FMT == QG_KV8_INT8 ? (float)(int8_t)b
+                                              : __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3))));
         }
-        store4(out + i * 16 + 4 * j, x);
+        if (i < words) store4(out + i * 4, x);
     }
 }
 
@@ -421,13 +432,13 @@ __global__ void values_kernel(const CacheView c, float* k_out, float* v_out, lon
 
 int launch_kv8_values(const qg_kv8_cache& c, float* k_out, float* v_out, const LaunchCtx& lc) {
     using namespace kv8;
-    const long long vecs = (long long)c.n_pages * c.n_kv_heads * c.page_size * c.head_dim / 16;
-    const long long grid = (vecs + 255) / 256;
+    const long long words = (long long)c.n_pages * c.n_kv_heads * c.page_size * c.head_dim / 4;
+    const long long grid = (words + 256 * VALUE_WORDS - 1) / (256 * VALUE_WORDS);
     if (grid > 0x7fffffffll) return QG_ERR_UNSUPPORTED;
     const dim3 g((unsigned)grid, 2);
     return c.format == QG_KV8_INT8
-               ? launch_kernel(values_kernel<QG_KV8_INT8>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, vecs, ilog2(c.head_dim))
-               : launch_kernel(values_kernel<QG_KV8_E4M3>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, vecs, ilog2(c.head_dim));
+               ? launch_kernel(values_kernel<QG_KV8_INT8>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, words, ilog2(c.head_dim))
+               : launch_kernel(values_kernel<QG_KV8_E4M3>, g, dim3(256), 0, lc, view_of(c), k_out, v_out, words, ilog2(c.head_dim));
 }
 
 int launch_kv8_append(const qg_kv8_cache& c, const qg_kv8_append_args& a, const LaunchCtx& lc) {
