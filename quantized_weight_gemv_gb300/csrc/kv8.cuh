@@ -118,6 +118,28 @@ __device__ __forceinline__ void load_values(const T* p, float (&x)[N]) {
     }
 }
 
+// ---------------------------------------------------------------- two fp32 values in one register pair
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+    return (unsigned long long)__float_as_uint(b) << 32 | __float_as_uint(a);
+}
+__device__ __forceinline__ float2 unpair(unsigned long long v) {
+    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 // ---------------------------------------------------------------- attention: what both kernels share
 // Weights are held as 2^(x - m + P_BITS): binary16 keeps 11 bits of a weight down to 2^-24 of the largest.
 constexpr float P_BITS = 10.0f;

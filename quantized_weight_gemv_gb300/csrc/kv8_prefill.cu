@@ -136,31 +136,9 @@ __device__ __forceinline__ void tmem_request8(uint32_t at, uint32_t (&v)[8]) {
 __device__ __forceinline__ void tmem_wait8(uint32_t (&v)[8]) {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : QG_X8(v, 0)::"memory");
 }
-// two fp32 lanes of one register pair
-__device__ __forceinline__ unsigned long long pair(float a, float b) {
-    return (unsigned long long)__float_as_uint(b) << 32 | __float_as_uint(a);
-}
-__device__ __forceinline__ float2 unpair(unsigned long long v) {
-    return make_float2(__uint_as_float((uint32_t)v), __uint_as_float((uint32_t)(v >> 32)));
-}
-__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
-    unsigned long long d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
-    unsigned long long d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ void tmem_load16(uint32_t at, uint32_t (&v)[16]) {
