@@ -318,7 +318,7 @@ int qgemv_chain(int bits, const qg_gemv_desc* descs, int count, const int* phase
  * A cache is a pool of pages of page_size tokens:
  *   k, v      : device uint8 [n_pages][n_kv_heads][page_size][head_dim], one code per value
  *   k_scale, v_scale : device fp32 [n_pages][n_kv_heads][page_size / scale_block]
- *   value     = scale of the (block of scale_block tokens, head) * code, the code an int8 in
+ *   value     = scale (>= 0) of the (block of scale_block tokens, head) * code, the code an int8 in
  *               [-127, 127] (QG_KV8_INT8) or an OCP 8-bit float (QG_KV8_E4M3)
  *   page_table : device int32 [batch][max_pages]; token j of sequence b is slot
  *               j % page_size of page page_table[b][j / page_size]
