@@ -372,6 +372,8 @@ typedef struct qg_kv8_cache {
  *     device tables [n_pos][rot_dim/2] (16-byte aligned) at row positions[t] (device int32
  *     [tokens]), or the token's cache position where positions is NULL.  Each product and
  *     sum is rounded to fp32 on its own.  cos and sin NULL: no rotation.  v is not rotated.
+ *     A row outside 0 .. n_pos - 1 leaves the token's key and query unrotated and sets 32 in
+ *     the error word.
  *   cache: per (block, head) and for k and v on their own, a = the largest finite |value| of
  *     the call's tokens in the block; the scale becomes s' = max(s, fl(a / qmax)) with qmax
  *     127 or 448, s being the stored scale, or 0 where this call holds the block's first

@@ -66,6 +66,14 @@ def test_cache_refusals(lib, kw, status):
     assert lib.kv8_attention(ctypes.byref(c), ctypes.byref(attention_args()), P(A), ws, 0, None) == status
 
 
+def test_values_refusals(lib):
+    c = ctypes.byref(cache())
+    assert lib.kv8_values(None, P(A), P(A), 0, None) == -1
+    assert lib.kv8_values(c, None, None, 0, None) == -1
+    assert lib.kv8_values(c, P(MIS), P(A), 0, None) == -2
+    assert lib.kv8_values(c, P(A), P(MIS), 0, None) == -2
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=3), -3), (dict(tokens=-1), -1), (dict(cu_tokens=None), -1), (dict(kv_len=None), -1), (dict(sin=None), -1),
     (dict(q_out=None), -1), (dict(q=None), -1), (dict(n_q_heads=0), -1), (dict(rope_style=2), -3), (dict(rot_dim=12), -1),
