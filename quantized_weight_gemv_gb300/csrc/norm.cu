@@ -9,12 +9,18 @@
 //   longer rows              : one CTA per row, 8 values a thread in 32 registers, so that
 //                              2048 threads of an SM have their loads in flight; above 8192
 //                              values 32 a thread, h being read after the first reduction
-// VEC: 16-byte accesses of eight consecutive values (n a multiple of 8, everything 16-byte
-// aligned); otherwise the same loop takes single values, a warp's neighbours side by side.
+// Access: ALIGNED, 16-byte accesses of eight consecutive values (n and strides multiples of 8,
+// everything 16-byte aligned).  SHIFTED, rows that start anywhere but all of a row's tensors at
+// the same place modulo eight values (contiguous rows of an odd n): whole chunks on the tensors'
+// 16-byte grid, the at most 15 values around them one to a thread, the weights moved into place
+// in registers.  SINGLE: single values, a warp's neighbours side by side (8191 x 1531 bfloat16:
+// 42.6 us, SHIFTED 28.6).
 // Measured and not kept (8191 x 2048 bfloat16, 23.6 us as it is, 5.6 TB/s): two rows to a CTA
 // 32.7 us, 16 values a thread 25.4 us (fp32 58.5 against 45.5 us), a CTA that walks over rows
 // with the next one's loads in flight 35.9 us, each for want of registers; a warp for rows of
 // 512 and 1024 (21.4 and 36.8 against 19.0 and 23.8 us for 16384 of them).
+#include <type_traits>
+
 #include "kv8.cuh"
 
 namespace qg {
@@ -33,9 +39,12 @@ struct NormParams {
     float eps, w_offset, res_scale, inv_n;
 };
 
-template <bool VEC, typename T>
+enum Access : int { SINGLE, ALIGNED, SHIFTED };
+
+// eight values of a row from `first` on (SINGLE: `step` apart, 0 past n)
+template <int A, typename T>
 __device__ __forceinline__ void load_chunk(const T* row, int first, int step, int n, float (&x)[8]) {
-    if constexpr (VEC && sizeof(T) == 4) {
+    if constexpr (A != SINGLE && sizeof(T) == 4) {
         // spelled out: as pairs of registers the compiler takes them in four 8-byte loads (58 against
         // 46 us for 8191 x 2048 in fp32)
 #pragma unroll
@@ -44,16 +53,49 @@ __device__ __forceinline__ void load_chunk(const T* row, int first, int step, in
                          : "=f"(x[4 * i]), "=f"(x[4 * i + 1]), "=f"(x[4 * i + 2]), "=f"(x[4 * i + 3])
                          : "l"(row + first + 4 * i)
                          : "memory");
-    } else if constexpr (VEC) {
+    } else if constexpr (A != SINGLE) {
         kv8::load8(row + first, x);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = first + e * step < n ? kv8::to_float(row[first + e * step]) : 0.0f;
     }
 }
-template <bool VEC, typename T>
+
+// v[0 .. N-1] <- v[by ..] for by = 0 or BY
+template <int BY, int N, int M>
+__device__ __forceinline__ void move_down(uint32_t (&v)[M], bool yes) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = yes && i + BY < M ? v[i + BY] : v[i];
+}
+// SHIFTED: eight weights from `first` on (base on a 16-byte boundary), out of the two 16-byte
+// groups of eight that hold them, moved into place by the bits of first % 8
+template <typename T>
+__device__ __forceinline__ void load_shifted(const T* row, int first, float (&x)[8]) {
+    constexpr int WORDS = sizeof(T) * 2;  // 32-bit words of eight values
+    const int by = first & 7;
+    uint32_t v[2 * WORDS];
+#pragma unroll
+    for (int i = 0; i < 2 * WORDS; i += 4) {
+        const uint4 q = *(reinterpret_cast<const uint4*>(row + first - by) + i / 4);
+        v[i] = q.x, v[i + 1] = q.y, v[i + 2] = q.z, v[i + 3] = q.w;
+    }
+    if constexpr (sizeof(T) == 4) {
+        move_down<4, 12>(v, by & 4);
+        move_down<2, 10>(v, by & 2);
+        move_down<1, 8>(v, by & 1);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = __uint_as_float(v[e]);
+    } else {
+        move_down<2, 6>(v, by & 4);
+        move_down<1, 5>(v, by & 2);
+        const T* tag = nullptr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) kv8::unpack2(tag, __funnelshift_r(v[i], v[i + 1], 16 * (by & 1)), x[2 * i], x[2 * i + 1]);
+    }
+}
+template <int A, typename T>
 __device__ __forceinline__ void store_chunk(T* row, int first, int step, int n, const float (&x)[8]) {
-    if constexpr (VEC) {
+    if constexpr (A != SINGLE) {
         kv8::store8(row + first, x);
     } else {
 #pragma unroll
@@ -78,8 +120,8 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 
 // IT chunks of eight values per thread, held as pairs (packed fp32 arithmetic: at 8191 x 2048
 // the scalar form issued 42 instructions a value and kept the issue slots 80 % busy)
-template <typename T, typename R, bool VEC, int IT, bool WARP>
-__global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC ? 2 : 1) norm_kernel(const NormParams p) {
+template <typename T, typename R, int A, int IT, bool WARP>
+__global__ void __launch_bounds__(WARP ? 128 : 1024, A != ALIGNED ? 1 : WARP ? 16 : IT == 1 ? 2 : 1) norm_kernel(const NormParams p) {
     __shared__ float red[2][32];
     pdl_wait();
     pdl_launch_dependents();
@@ -97,14 +139,30 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC 
     using kv8::mul2;
     using kv8::pair;
 
-    // chunk i: eight values from place(i), `step` apart; n / 8 whole chunks where VEC
-    const int step = VEC ? 1 : threads;
-    auto place = [&](int i) { return VEC ? (i * threads + tid) * 8 : i * threads * 8 + tid; };
-    auto load = [&](const auto* from, int at, Pair (&x)[4]) {
-        float v[8];
-        load_chunk<VEC>(from, at, step, n, v);
+    // chunk i: eight values from place(i) on, where the thread has one (SHIFTED: chunks whose
+    // weights' two groups lie within n; edge: the value beside them that this thread takes)
+    const int step = A == SINGLE ? threads : 1;
+    const int head = A == SHIFTED ? (int)(-(reinterpret_cast<uintptr_t>(h) / sizeof(R)) & 7) : 0;
+    const int chunks = A == SHIFTED && n >= 16 ? n / 8 - 1 : 0;
+    const int edge = A != SHIFTED || tid >= n - 8 * chunks ? -1 : chunks == 0 || tid < head ? tid : tid + 8 * chunks;
+    auto place = [&](int i) { return A == SINGLE ? i * threads * 8 + tid : head + (i * threads + tid) * 8; };
+    auto mine = [&](int i) { return A == SHIFTED ? i * threads + tid < chunks : place(i) < n; };
+    auto pairs = [&](const float (&v)[8], Pair (&x)[4]) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = pair(v[2 * e], v[2 * e + 1]);
+    };
+    auto load = [&](const auto* from, int at, Pair (&x)[4]) {
+        float v[8];
+        load_chunk<A>(from, at, step, n, v);
+        pairs(v, x);
+    };
+    auto load_weights = [&](const T* from, int at, Pair (&x)[4]) {
+        float v[8];
+        if constexpr (A == SHIFTED)
+            load_shifted(from, at, v);
+        else
+            load_chunk<A>(from, at, step, n, v);
+        pairs(v, x);
     };
     auto store = [&](auto* to, int at, const Pair (&x)[4]) {
         float v[8];
@@ -113,25 +171,33 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC 
             const float2 f = kv8::unpair(x[e]);
             v[2 * e] = f.x, v[2 * e + 1] = f.y;
         }
-        store_chunk<VEC>(to, at, step, n, v);
+        store_chunk<A>(to, at, step, n, v);
     };
+    auto one = [&](const T* from) { return edge >= 0 ? kv8::to_float(from[edge]) : 0.0f; };
     auto both = [](Pair s) {
         const float2 f = kv8::unpair(s);
         return f.x + f.y;
     };
+    const T* y = p.y ? reinterpret_cast<const T*>(p.y) + row * p.y_stride : nullptr;
+    R* h_out = p.h_out ? reinterpret_cast<R*>(p.h_out) + row * p.h_out_stride : nullptr;
 
     Pair a[IT][4], hv[IT][4];
+    float ea = 0.0f, eh = 0.0f;  // the edge value
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int at = place(i);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[i][e] = 0ull;
-        if (at < n && p.y) load(reinterpret_cast<const T*>(p.y) + row * p.y_stride, at, a[i]);
+        if (mine(i) && y) load(y, at, a[i]);
         if (IT == 1) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) hv[i][e] = 0ull;
-            if (at < n) load(h, at, hv[i]);
+            if (mine(i)) load(h, at, hv[i]);
         }
+    }
+    if constexpr (A == SHIFTED) {
+        if (y) ea = one(y);
+        if (edge >= 0) eh = kv8::to_float(h[edge]);
     }
     float r = 1.0f;
     if (wpost) {
@@ -140,7 +206,7 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC 
         for (int i = 0; i < IT; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) s = fma2(a[i][e], a[i][e], s);
-        r = rsqrtf(fmaf(row_sum<WARP>(both(s), red[0]), p.inv_n, p.eps));
+        r = rsqrtf(fmaf(row_sum<WARP>(fmaf(ea, ea, both(s)), red[0]), p.inv_n, p.eps));
     }
     Pair s = 0ull;
     {
@@ -148,16 +214,19 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC 
 #pragma unroll
         for (int i = 0; i < IT; ++i) {
             const int at = place(i);
-            if (at >= n) continue;
+            if (!mine(i)) continue;
             Pair c[4];
             if (IT > 1) load(h, at, hv[i]);
             if (wpost) {
-                load(wpost, at, c);
+                load_weights(wpost, at, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a[i][e] = mul2(a[i][e], fma2(c[e], r2, off));
             }
             if (gate) {
-                load(gate + row * p.gate_stride, at, c);
+                if (p.gate_stride != 0)
+                    load(gate + row * p.gate_stride, at, c);
+                else
+                    load_weights(gate, at, c);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) a[i][e] = mul2(a[i][e], c[e]);
             }
@@ -166,43 +235,72 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024, WARP ? 16 : IT == 1 && VEC 
                 a[i][e] = mul2(add2(hv[i][e], a[i][e]), scale);  // h'
                 s = fma2(a[i][e], a[i][e], s);
             }
-            if (p.h_out) store(reinterpret_cast<R*>(p.h_out) + row * p.h_out_stride, at, a[i]);
+            if (h_out) store(h_out, at, a[i]);
+        }
+        if constexpr (A == SHIFTED) {
+            if (wpost) ea *= fmaf(one(wpost), r, r * p.w_offset);
+            if (gate) ea *= one(gate + row * p.gate_stride);
+            ea = (eh + ea) * p.res_scale;
+            if (h_out && edge >= 0) kv8::from_float(ea, h_out[edge]);
         }
     }
     if (!wpre) return;
-    r = rsqrtf(fmaf(row_sum<WARP>(both(s), red[1]), p.inv_n, p.eps));
+    r = rsqrtf(fmaf(row_sum<WARP>(fmaf(ea, ea, both(s)), red[1]), p.inv_n, p.eps));
     const Pair r2 = pair(r, r), off = pair(r * p.w_offset, r * p.w_offset);
+    T* z = reinterpret_cast<T*>(p.z) + row * p.z_stride;
 #pragma unroll
     for (int i = 0; i < IT; ++i) {
         const int at = place(i);
-        if (at >= n) continue;
+        if (!mine(i)) continue;
         Pair c[4];
-        load(wpre, at, c);
+        load_weights(wpre, at, c);
 #pragma unroll
         for (int e = 0; e < 4; ++e) a[i][e] = mul2(a[i][e], fma2(c[e], r2, off));
-        store(reinterpret_cast<T*>(p.z) + row * p.z_stride, at, a[i]);
+        store(z, at, a[i]);
+    }
+    if constexpr (A == SHIFTED) {
+        const float w = one(wpre);
+        if (edge >= 0) kv8::from_float(ea * fmaf(w, r, r * p.w_offset), z[edge]);
     }
 }
 
-template <typename T, typename R, bool VEC>
+template <typename T, typename R, int A>
 static int launch_rows(const NormParams& p, const LaunchCtx& lc) {
-    if (p.n <= 256) return launch_kernel(norm_kernel<T, R, VEC, 1, true>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, lc, p);
-    const int it = p.n > 8192 ? 4 : 1;
-    const dim3 grid((unsigned)p.rows), block((unsigned)(((p.n + 8 * it - 1) / (8 * it) + 31) & ~31));
-    return it == 4 ? launch_kernel(norm_kernel<T, R, VEC, 4, false>, grid, block, 0, lc, p)
-                   : launch_kernel(norm_kernel<T, R, VEC, 1, false>, grid, block, 0, lc, p);
+    const int n = p.n;
+    if (n <= 256) return launch_kernel(norm_kernel<T, R, A, 1, true>, dim3((unsigned)((p.rows + 3) / 4)), dim3(128), 0, lc, p);
+    const int it = n > 8192 ? 4 : 1;
+    const dim3 grid((unsigned)p.rows), block((unsigned)(((n + 8 * it - 1) / (8 * it) + 31) & ~31));
+    return it == 4 ? launch_kernel(norm_kernel<T, R, A, 4, false>, grid, block, 0, lc, p)
+                   : launch_kernel(norm_kernel<T, R, A, 1, false>, grid, block, 0, lc, p);
 }
 
 template <typename T, typename R>
 static int launch_types(const NormParams& p, const LaunchCtx& lc) {
-    auto rows16 = [](const void* q, long long stride, size_t size) {
-        return !q || (((reinterpret_cast<uintptr_t>(q) | (uintptr_t)(stride * (long long)size)) & 15u) == 0);
+    struct Rows {
+        const void* at;
+        long long stride;
+        size_t size;
     };
     const size_t t = sizeof(T), r = sizeof(R);
-    const bool vec = p.n % 8 == 0 && rows16(p.y, p.y_stride, t) && rows16(p.h, p.h_stride, r) &&
-                     rows16(p.gate, p.gate_stride, t) && rows16(p.w_post, 0, t) && rows16(p.w_pre, 0, t) &&
-                     rows16(p.h_out, p.h_out_stride, r) && rows16(p.z, p.z_stride, t);
-    return vec ? launch_rows<T, R, true>(p, lc) : launch_rows<T, R, false>(p, lc);
+    const Rows rows[] = {{p.h, p.h_stride, r}, {p.y, p.y_stride, t}, {p.h_out, p.h_out_stride, r}, {p.z, p.z_stride, t},
+                         {p.gate_stride ? p.gate : nullptr, p.gate_stride, t}};
+    const void* once[] = {p.w_post, p.w_pre, p.gate_stride ? nullptr : p.gate};
+    // every row tensor's place modulo eight values (one that holds a single row has no stride to speak of)
+    auto place = [&](const Rows& x, int row) {
+        return (reinterpret_cast<uintptr_t>(x.at) / x.size + (uintptr_t)(row ? x.stride : 0)) & 7;
+    };
+    bool same = true, aligned = p.n % 8 == 0;
+    for (const Rows& x : rows) {
+        if (!x.at) continue;
+        for (int row = 0; row < (p.rows > 1 ? 2 : 1); ++row) {
+            same = same && place(x, row) == place(rows[0], row);
+            aligned = aligned && place(x, row) == 0;
+        }
+    }
+    for (const void* x : once)
+        if (x && (reinterpret_cast<uintptr_t>(x) & 15u) != 0) aligned = same = false;
+    if (aligned) return launch_rows<T, R, ALIGNED>(p, lc);
+    return same ? launch_rows<T, R, SHIFTED>(p, lc) : launch_rows<T, R, SINGLE>(p, lc);
 }
 
 }  // namespace norm
