@@ -306,10 +306,10 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         for (int o = 16; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         if (lane == 0 && top) atomicMax(&v_top, top);
     }
-    if (warp < 8) {
-        constexpr int PER = D / 32, BATCH = 8;
+    {
+        constexpr int PER = D / 32, BATCH = 8, OWN = RR / (PF_THREADS / 32);  // a warp's rows
         const float sign = p.scale < 0.0f ? -1.0f : 1.0f;  // the row factor stays positive
-        for (int r0 = warp * (RR / 8); r0 < (warp + 1) * (RR / 8); r0 += BATCH) {
+        for (int r0 = warp * OWN; r0 < (warp + 1) * OWN; r0 += BATCH) {
             float x[BATCH][PER];
 #pragma unroll
             for (int i = 0; i < BATCH; ++i) {
