@@ -307,48 +307,47 @@ __global__ void __launch_bounds__(PF_THREADS, 1) prefill_kernel(const AttnParams
         if (lane == 0 && top) atomicMax(&v_top, top);
     }
     {
-        constexpr int PER = D / 32, BATCH = 8, OWN = RR / (PF_THREADS / 32);  // a warp's rows
+        constexpr int PER = D / 32, OWN = RR / (PF_THREADS / 32);  // a warp's rows, loaded all at once
         const float sign = p.scale < 0.0f ? -1.0f : 1.0f;  // the row factor stays positive
-        for (int r0 = warp * OWN; r0 < (warp + 1) * OWN; r0 += BATCH) {
-            float x[BATCH][PER];
+        const int r0 = warp * OWN;
+        float x[OWN][PER];
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
+        for (int i = 0; i < OWN; ++i) {
 #pragma unroll
-                for (int e = 0; e < PER; ++e) x[i][e] = 0.0f;
-                if (r0 + i < rows) {
-                    const unsigned char* at = row_at(p.q, p.q_stride, r0 + i) + lane * PER * esize;
-                    if constexpr (PIECES == 2)
-                        load_values(reinterpret_cast<const float*>(at), x[i]);
-                    else if (p.dtype == QG_DTYPE_F16)
-                        load_values(reinterpret_cast<const __half*>(at), x[i]);
-                    else
-                        load_values(reinterpret_cast<const __nv_bfloat16*>(at), x[i]);
-                }
+            for (int e = 0; e < PER; ++e) x[i][e] = 0.0f;
+            if (r0 + i < rows) {
+                const unsigned char* at = row_at(p.q, p.q_stride, r0 + i) + lane * PER * esize;
+                if constexpr (PIECES == 2)
+                    load_values(reinterpret_cast<const float*>(at), x[i]);
+                else if (p.dtype == QG_DTYPE_F16)
+                    load_values(reinterpret_cast<const __half*>(at), x[i]);
+                else
+                    load_values(reinterpret_cast<const __nv_bfloat16*>(at), x[i]);
             }
+        }
 #pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-                const int r = r0 + i, rt = r / PF_ROWS, rr = r % PF_ROWS;
-                float a = 0.0f;
+        for (int i = 0; i < OWN; ++i) {
+            const int r = r0 + i, rt = r / PF_ROWS, rr = r % PF_ROWS;
+            float a = 0.0f;
 #pragma unroll
-                for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[i][e]));
+            for (int e = 0; e < PER; ++e) a = fmaxf(a, fabsf(x[i][e]));
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
-                const float down = ldexpf(sign, -ex);
+            for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const int ex = a > 0.0f ? (int)(__float_as_uint(a) >> 23) - 126 : 0;  // a < 2^ex
+            const float down = ldexpf(sign, -ex);
 #pragma unroll
-                for (int e = 0; e < PER; e += 2) {
-                    const int d = lane * PER + e;
-                    const float u = x[i][e] * down, v = x[i][e + 1] * down;
-                    const __half2 hi2 = __floats2half2_rn(u, v);
-                    unsigned char* at = qs + rt * PIECES * C::Q_BYTES + (d >> 6) * (PF_ROWS * 128) + rr * 128 +
-                                        ((((d & 63) >> 3) ^ (rr & 7)) << 4) + (d & 7) * 2;
-                    *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(&hi2);
-                    if constexpr (PIECES == 2)
-                        *reinterpret_cast<uint32_t*>(at + C::Q_BYTES) = half2_bits(u - __low2float(hi2), v - __high2float(hi2));
-                }
-                if (lane == 0)
-                    row_factor[r] = ldexpf(fabsf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f), ex);
+            for (int e = 0; e < PER; e += 2) {
+                const int d = lane * PER + e;
+                const float u = x[i][e] * down, v = x[i][e + 1] * down;
+                const __half2 hi2 = __floats2half2_rn(u, v);
+                unsigned char* at = qs + rt * PIECES * C::Q_BYTES + (d >> 6) * (PF_ROWS * 128) + rr * 128 +
+                                    ((((d & 63) >> 3) ^ (rr & 7)) << 4) + (d & 7) * 2;
+                *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(&hi2);
+                if constexpr (PIECES == 2)
+                    *reinterpret_cast<uint32_t*>(at + C::Q_BYTES) = half2_bits(u - __low2float(hi2), v - __high2float(hi2));
             }
+            if (lane == 0)
+                row_factor[r] = ldexpf(fabsf(p.softcap > 0.0f ? p.scale / p.softcap : p.scale * 1.44269504088896f), ex);
         }
         fence_async_smem();
     }
