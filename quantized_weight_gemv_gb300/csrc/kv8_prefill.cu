@@ -8,7 +8,8 @@
 // The cache's codes are exact in binary16, so K and V are widened without rounding and the
 // block scales multiply afterwards: K's onto the score, V's (relative to the largest power of
 // two among the CTA's blocks) onto P.  Queries are brought to [-1, 1] by a power of two per
-// row; fp32 queries and weights enter as two binary16 pieces, two products each.
+// row (all 16 warps at the start: 161 us for 2048 tokens over 8192, eight of them 169); fp32
+// queries and weights enter as two binary16 pieces, two products each.
 //
 // Roles (16 warps): one warpgroup per row tile does the softmax, a thread per row; four warps
 // widen the next tile's K codes from registers into the 128-byte-swizzled K-major tiles that
